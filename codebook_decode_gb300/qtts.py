@@ -25,6 +25,8 @@ QTTS_E_DEVICE = -10
 QTTS_E_TIMEOUT = -11
 (QTTS_DEV_OK, QTTS_DEV_BAD_SESSION, QTTS_DEV_BAD_PAGE, QTTS_DEV_BAD_SAMPLING, QTTS_DEV_BAD_CODE,
  QTTS_DEV_TIMEOUT) = range(6)
+QTTS_DTYPE_BF16 = 0
+QTTS_DTYPE_F32 = 1
 QTTS_OPT_STEPWISE = 1
 QTTS_OPT_TRACE = 3
 QTTS_OPT_RING_SLOTS = 4
@@ -65,6 +67,12 @@ class Rng(C.Structure):
     _fields_ = [("key0", C.c_uint32), ("key1", C.c_uint32), ("frame_ctr", C.c_uint32), ("reserved", C.c_uint32)]
 
 
+class Kv8Config(C.Structure):
+    _fields_ = [("n_layers", C.c_int32), ("n_q_heads", C.c_int32), ("n_kv_heads", C.c_int32),
+                ("head_dim", C.c_int32), ("rope_theta", C.c_float), ("page_size", C.c_int32),
+                ("max_batch", C.c_int32), ("max_context", C.c_int32), ("pool_pages", C.c_int32)]
+
+
 _lib = None
 _P = C.c_void_p
 
@@ -96,6 +104,18 @@ SIGNATURES = [
     ("qtts_set_option", C.c_int, [_P, C.c_int, C.c_int]),
     ("qtts_frame_weight_bytes", C.c_int, [_P, C.POINTER(C.c_int64)]),
     ("qtts_frame_trace", C.c_int, [_P, _P, C.c_int]),
+    ("qtts_kv8_last_error", C.c_char_p, [_P]),
+    ("qtts_kv8_create", C.c_int, [C.POINTER(Kv8Config), C.c_int, C.POINTER(_P)]),
+    ("qtts_kv8_destroy", None, [_P]),
+    ("qtts_kv8_alloc_pages", C.c_int, [_P, C.c_int, _P]),
+    ("qtts_kv8_free_pages", C.c_int, [_P, C.c_int, _P]),
+    ("qtts_kv8_free_count", C.c_int, [_P]),
+    ("qtts_kv8_append", C.c_int, [_P] + [C.c_int] * 4 + [_P] * 3 + [C.c_int, _P, C.c_int64, _P, C.c_int64, _P]),
+    ("qtts_kv8_workspace_bytes", C.c_int64, [_P]),
+    ("qtts_kv8_attention", C.c_int, [_P] + [C.c_int] * 4 + [_P] * 3 + [C.c_int, _P, C.c_int64, C.c_float, _P,
+                                                                       C.c_int64, _P, _P]),
+    ("qtts_kv8_read", C.c_int, [_P] + [C.c_int] * 4 + [_P] * 3 + [C.c_int, _P, _P, _P]),
+    ("qtts_kv8_status", C.c_int, [_P, C.POINTER(C.c_int)]),
 ]
 
 
@@ -282,3 +302,64 @@ def qtts_frame_trace(m, host_u64):
     if n < 0:
         _check(m, n)
     return n
+
+
+def _check_kv8(c, rc):
+    if rc != QTTS_OK:
+        raise QttsError(rc, load_library().qtts_kv8_last_error(c).decode())
+    return rc
+
+
+def qtts_kv8_create(cfg, device=0):
+    c = C.c_void_p()
+    _check_kv8(None, load_library().qtts_kv8_create(C.byref(cfg), device, C.byref(c)))
+    return c
+
+
+def qtts_kv8_destroy(c):
+    load_library().qtts_kv8_destroy(c)
+
+
+def qtts_kv8_alloc_pages(c, ids_host):
+    return _check_kv8(c, load_library().qtts_kv8_alloc_pages(c, len(ids_host), ptr(ids_host)))
+
+
+def qtts_kv8_free_pages(c, ids_host):
+    return _check_kv8(c, load_library().qtts_kv8_free_pages(c, len(ids_host), ptr(ids_host)))
+
+
+def qtts_kv8_free_count(c):
+    return load_library().qtts_kv8_free_count(c)
+
+
+def qtts_kv8_append(c, layer, B, n_rows, max_new, row_start, kv_len, block_tables, bt_stride, k, k_stride, v,
+                    v_stride, stream=None):
+    return _check_kv8(c, load_library().qtts_kv8_append(
+        c, layer, B, n_rows, max_new, ptr(row_start), ptr(kv_len), ptr(block_tables), bt_stride, ptr(k), k_stride,
+        ptr(v), v_stride, _stream(stream)))
+
+
+def qtts_kv8_workspace_bytes(c):
+    return load_library().qtts_kv8_workspace_bytes(c)
+
+
+def qtts_kv8_attention(c, layer, B, n_rows, max_new, row_start, kv_len, block_tables, bt_stride, q, q_stride, scale,
+                       out, out_stride, workspace, stream=None):
+    return _check_kv8(c, load_library().qtts_kv8_attention(
+        c, layer, B, n_rows, max_new, ptr(row_start), ptr(kv_len), ptr(block_tables), bt_stride, ptr(q), q_stride,
+        scale, ptr(out), out_stride, ptr(workspace), _stream(stream)))
+
+
+def qtts_kv8_read(c, layer, B, n_rows, max_new, row_start, pos0, block_tables, bt_stride, k_out, v_out, stream=None):
+    return _check_kv8(c, load_library().qtts_kv8_read(
+        c, layer, B, n_rows, max_new, ptr(row_start), ptr(pos0), ptr(block_tables), bt_stride, ptr(k_out),
+        ptr(v_out), _stream(stream)))
+
+
+def qtts_kv8_status(c, raise_on_error=True):
+    """Returns (rc, device error word); the word is cleared by the call."""
+    e = C.c_int(0)
+    rc = load_library().qtts_kv8_status(c, C.byref(e))
+    if raise_on_error:
+        _check_kv8(c, rc)
+    return rc, e.value

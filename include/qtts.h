@@ -73,6 +73,7 @@ extern "C" {
 #define QTTS_DEV_TIMEOUT 5      /* a device-side wait (activation words, weight ring, tensor-path barriers) ran out its limit */
 
 #define QTTS_DTYPE_BF16 0
+#define QTTS_DTYPE_F32 1
 
 typedef struct qtts_model qtts_model;
 
@@ -386,6 +387,99 @@ int qtts_frame_trace(qtts_model* m, uint64_t* host, int capacity);
 /* Bytes of weights one frame streams (the roofline's numerator, without KV):
  * every GEMM weight once per pass that uses it, in the current precision. */
 int qtts_frame_weight_bytes(const qtts_model* m, int64_t* bytes);
+
+/* ---------------------------------------------------------------------------
+ * An 8-bit paged K/V cache and attention over it. A cache of its own, beside
+ * the model's bf16 pool: half the bytes per token, and contexts up to 262144.
+ *
+ * A block is one page (16 tokens) of one kv head's K or V: int8 codes and one
+ * fp32 scale. The scale is max|x| / 127 over the values the block was given
+ * (below 2^-100 it is 0 and the block reads as zeros; a NaN or an
+ * infinity among the values makes it NaN, so that whatever reads the block
+ * shows it), a code is round-half-even(x * (1 / scale)) clamped to
+ * [-127, 127]. Appending to a block that holds tokens keeps the larger of its
+ * scale and the new values' one; where it grows, the codes already there
+ * become round-half-even(code * (old scale / new scale)). Scales, reciprocals,
+ * ratios and these products are binary32. A row that lands on
+ * slot 0 of a page starts its blocks anew, so freed pages need no clearing.
+ *
+ * Calls take a batch of B sessions with their rows packed: session b has the
+ * rows row_start[b] .. row_start[b + 1] - 1 (device [B + 1]; NULL: exactly one
+ * row per session, n_rows = B, max_new = 1), n_rows is the number of rows that
+ * the row arrays hold, and no session has more than max_new of them. kv_len
+ * (device [B]) is the number of tokens before a session's first row, which so
+ * has position kv_len[b]; nothing advances it: the caller does, once per step
+ * after the last layer. A session without rows, or with a negative kv_len, is
+ * skipped, and rows behind row_start[B] are left as they are: a captured graph
+ * can run a batch that is not full. block_tables as in qtts_frame_step.
+ * All array pointers are device memory; row arrays are bf16, 8-byte aligned,
+ * with a stride between rows in elements (a multiple of 4), so that Q, K and V
+ * may be slices of one projection's output. Calls are asynchronous on
+ * `stream`, allocate nothing and can be captured into a graph; the caller's
+ * current device is left as it was.
+ * Device-side checks: a session whose rows do not fit row_start, max_new,
+ * max_context or its block table is skipped (QTTS_DEV_BAD_SESSION); a page id
+ * outside the pool is not written, and what attention gives for that session
+ * is unspecified (QTTS_DEV_BAD_PAGE). Other sessions go on. The first error is
+ * kept until qtts_kv8_status reads it.
+ * ------------------------------------------------------------------------- */
+typedef struct qtts_kv8 qtts_kv8;
+
+typedef struct {
+  int32_t n_layers, n_q_heads, n_kv_heads;
+  int32_t head_dim;     /* 64 or 128 */
+  float rope_theta;     /* 0: keys and queries are not rotated */
+  int32_t page_size;    /* must be 16 */
+  int32_t max_batch;    /* 1..1024 */
+  int32_t max_context;  /* 1..262144; the rotation table holds max_context * head_dim * 4 bytes */
+  int32_t pool_pages;   /* pages of every layer */
+} qtts_kv8_config;
+
+const char* qtts_kv8_last_error(const qtts_kv8* c); /* c may be NULL for create errors */
+int qtts_kv8_create(const qtts_kv8_config* cfg, int device, qtts_kv8** out);
+void qtts_kv8_destroy(qtts_kv8* c);
+
+/* The page pool, as qtts_kv_alloc_pages and its kind. */
+int qtts_kv8_alloc_pages(qtts_kv8* c, int n, int32_t* ids_host);
+int qtts_kv8_free_pages(qtts_kv8* c, int n, const int32_t* ids_host);
+int qtts_kv8_free_count(const qtts_kv8* c);
+
+/* Append n rows per session to layer `layer`: K rotated by its position
+ * (rotate-half pairs (i, i + d/2) by pos * theta^(-2i/d), angles in double,
+ * products in fp32), then K and V quantised into the pages. k, v: rows of
+ * [n_kv_heads][head_dim]. No two sessions of a call may append to the same
+ * page (they would write the same block); sharing pages that are only read is
+ * fine. */
+int qtts_kv8_append(qtts_kv8* c, int layer, int B, int n_rows, int max_new, const int32_t* row_start,
+                    const int32_t* kv_len, const int32_t* block_tables, int bt_stride, const uint16_t* k,
+                    int64_t k_stride, const uint16_t* v, int64_t v_stride, void* stream);
+
+/* Causal attention of rows already appended: row i of session b, at position
+ * kv_len[b] + i, sees positions 0 .. kv_len[b] + i:
+ *   out = sum_j softmax_j(scale * q_rot . K_j) V_j
+ * q: rows of [n_q_heads][head_dim], not yet rotated (they are rotated like K
+ * here, in fp32); out: the same shape. Query head h reads kv head
+ * h / (n_q_heads / n_kv_heads). workspace: qtts_kv8_workspace_bytes of device
+ * memory, 16-byte aligned, zeroed once before its first call and left ready
+ * for the next one; calls that may overlap (on several streams, or captured
+ * into graphs that may run at once) need one each. Results do not depend on
+ * timing. */
+int64_t qtts_kv8_workspace_bytes(const qtts_kv8* c);
+int qtts_kv8_attention(qtts_kv8* c, int layer, int B, int n_rows, int max_new, const int32_t* row_start,
+                       const int32_t* kv_len, const int32_t* block_tables, int bt_stride, const uint16_t* q,
+                       int64_t q_stride, float scale, uint16_t* out, int64_t out_stride, void* workspace,
+                       void* stream);
+
+/* Read positions pos0[b] .. of every session back as bf16 (code * scale,
+ * rounded once), rows packed as above: k_out, v_out [n_rows][n_kv_heads]
+ * [head_dim]. K as it is held, rotated. */
+int qtts_kv8_read(qtts_kv8* c, int layer, int B, int n_rows, int max_new, const int32_t* row_start,
+                  const int32_t* pos0, const int32_t* block_tables, int bt_stride, uint16_t* k_out, uint16_t* v_out,
+                  void* stream);
+
+/* Wait for the device, then read and clear the cache's error word
+ * (QTTS_DEV_*). Returns QTTS_E_DEVICE / QTTS_E_TIMEOUT when it was set. */
+int qtts_kv8_status(qtts_kv8* c, int* device_err);
 
 #ifdef __cplusplus
 }
