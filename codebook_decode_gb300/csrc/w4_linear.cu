@@ -1,0 +1,500 @@
+// w4_linear.cu -- products of up to 64 activation rows with 4-bit weights:
+// y[m][n] = sum_k x[m][k] * code[n][k] * scale[n][k / group].
+//
+// Bound by the weights' bytes (half a byte each) for few rows. The weights are
+// the A operand of mma.sync m16n8k16 (16 output columns of the layer per
+// tile), the activations the B operand (8 rows per n-tile), so that one
+// activation row pads to 8, not to 16 or 128. Codes are exact in bf16 and are
+// widened in registers (4 bits under the exponent of 2^7, minus 136); a
+// group's scale multiplies its fp32 partial sums, so nothing is rounded before
+// the result.
+//
+// Weights in memory: tiles of 16 rows x 64 k, one lane's 32 codes together
+// (512 contiguous bytes a tile, tiles of a row block in k order): word e of
+// lane (g, t) holds for rows g and g + 8 the codes of
+//   k = 32 (e / 2) + 8 t + 4 (e % 2) + 0..3
+// as the nibbles of one MMA's four A registers. Every MMA so lies inside 32
+// consecutive k and one group, and a lane's activations are 16 contiguous
+// bytes. Scales follow the same order: [row block][k tile][g][row half, 32-k
+// half] for groups of 32, [row block][group][g][row half] above.
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdarg>
+#include <cstdio>
+#include <new>
+
+#include "device_util.cuh"
+#include "qtts_internal.h"
+
+struct qtts_w4 {
+  int N = 0, K = 0, group = 0, device = 0, G = 0;
+  int RB = 0, KT = 0;  // row blocks of 16, k tiles of 64
+  char err[256] = {};
+  uint4* codes = nullptr;      // [RB][KT][32 lanes]
+  uint16_t* scales = nullptr;  // [RB][units][16 or 32]
+  bool loaded = false;
+};
+
+namespace qtts {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kW4Rows = 16, kW4K = 64, kW4MaxM = 64;
+constexpr int kW4Warps = 8, kW4Threads = 32 * kW4Warps;
+
+// scales of one row block and k tile of 64 (groups of 32), or of one group
+__host__ __device__ __forceinline__ int scale_units(int KT, int K, int group) { return group == 32 ? KT : K / group; }
+// place of (row r of the block, 32-k half or 0) within its unit
+__device__ __forceinline__ int scale_slot(int r, int half, int group) {
+  return group == 32 ? (r & 7) * 4 + (r >> 3) * 2 + half : (r & 7) * 2 + (r >> 3);
+}
+__device__ __forceinline__ size_t scale_at(int n, int grp, int KT, int K, int group) {
+  const int units = scale_units(KT, K, group);
+  const size_t rb = n / kW4Rows;
+  return group == 32 ? (rb * units + grp / 2) * 32 + scale_slot(n % kW4Rows, grp & 1, group)
+                     : (rb * units + grp) * 16 + scale_slot(n % kW4Rows, 0, group);
+}
+// k of nibble j (0..3) of MMA e of a tile, for lane quad position t
+__device__ __forceinline__ int k_of(int e, int t, int j) { return 32 * (e >> 1) + 8 * t + 4 * (e & 1) + j; }
+
+// ---- load time: quantise, pack, unpack (natural order [N][K], [N][K / group])
+
+__global__ void w4_quantize_kernel(const uint16_t* w, int N, int K, int group, int8_t* q, uint16_t* s) {
+  const int groups = K / group, lane = threadIdx.x & 31;
+  const long long total = (long long)N * groups;
+  for (long long i = blockIdx.x * (blockDim.x / 32ll) + threadIdx.x / 32; i < total;
+       i += gridDim.x * (blockDim.x / 32ll)) {
+    const uint16_t* src = w + i * group;
+    uint32_t mx = 0;
+    for (int k = lane; k < group; k += 32) mx = max(mx, (uint32_t)src[k] & 0x7fffu);
+    mx = __reduce_max_sync(0xffffffffu, mx);
+    uint16_t sb = mx >= 0x7f80u ? (uint16_t)0x7fffu : f2bf(bf2f(mx) / 7.f);
+    if (sb < 0x0080u) sb = 0;  // below the normal numbers
+    const float sc = bf2f(sb);
+    for (int k = lane; k < group; k += 32) {
+      const float x = sb ? bf2f(src[k]) / sc : 0.f;
+      q[i * group + k] = (int8_t)__float2int_rn(fminf(fmaxf(x, -7.f), 7.f));
+    }
+    if (lane == 0) s[i] = sb;
+  }
+}
+
+__global__ void w4_pack_kernel(const int8_t* q, const uint16_t* s, int N, int K, int group, int RB, int KT,
+                               uint4* codes, uint16_t* scales, int* bad) {
+  const long long total = (long long)RB * KT * 32;
+  const int groups = K / group;
+  for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < total;
+       i += gridDim.x * (long long)blockDim.x) {
+    const int lane = i & 31, g = lane >> 2, t = lane & 3;
+    const int kt = (int)(i / 32 % KT), rb = (int)(i / 32 / KT);
+    uint32_t w[4];
+    for (int e = 0; e < 4; ++e) {
+      w[e] = 0;
+      for (int a = 0; a < 4; ++a)  // A register a: row g or g + 8, nibbles 2 (a / 2), 2 (a / 2) + 1
+        for (int h = 0; h < 2; ++h) {
+          const int n = rb * kW4Rows + g + 8 * (a & 1), k = kt * kW4K + k_of(e, t, 2 * (a >> 1) + h);
+          int c = 0;
+          if (n < N && k < K) c = q[(size_t)n * K + k];
+          if (c < -8 || c > 7) *bad = 1;
+          w[e] |= (uint32_t)((c + 8) & 15) << (4 * a + 16 * h);
+        }
+    }
+    codes[i] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  const long long ns = (long long)N * groups;
+  for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < ns; i += gridDim.x * (long long)blockDim.x)
+    scales[scale_at((int)(i / groups), (int)(i % groups), KT, K, group)] = s[i];
+}
+
+__global__ void w4_unpack_kernel(const uint4* codes, const uint16_t* scales, int N, int K, int group, int KT,
+                                 int8_t* q, uint16_t* s) {
+  const long long total = (long long)N * K;
+  const int groups = K / group;
+  for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < total;
+       i += gridDim.x * (long long)blockDim.x) {
+    const int n = (int)(i / K), k = (int)(i % K);
+    const int r = n % kW4Rows, kk = k % kW4K;
+    const int e = (kk >> 5) * 2 + ((kk >> 2) & 1), t = (kk >> 3) & 3, j = kk & 3;
+    const uint4 v = codes[((size_t)(n / kW4Rows) * KT + k / kW4K) * 32 + (r & 7) * 4 + t];
+    const uint32_t w = e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w;
+    const int a = (r >> 3) + 2 * (j >> 1);
+    q[i] = (int8_t)((int)(w >> (4 * a + 16 * (j & 1)) & 15u) - 8);
+  }
+  const long long ns = (long long)N * groups;
+  for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < ns; i += gridDim.x * (long long)blockDim.x)
+    s[i] = scales[scale_at((int)(i / groups), (int)(i % groups), KT, K, group)];
+}
+
+// ---- the product
+
+struct W4Args {
+  const uint4* codes;
+  const uint16_t* scales;
+  int N, K, RB, KT, group, sunits;
+  int M;
+  const uint16_t* x;
+  int64_t x_stride;
+  void* y;
+  int64_t y_stride;
+  int y_f32;
+  int rw;  // warps along the row blocks; kW4Warps / rw along k
+};
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two codes to a bf16 pair: 4 bits under the exponent of 2^7 are 128 + code +
+// 8, minus 136 the code itself, exactly.
+__device__ __forceinline__ uint32_t widen4(uint32_t w) {
+  uint32_t r;
+  const uint32_t off = 0x43084308u;  // 136, 136
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"((w & 0x000f000fu) | 0x43004300u), "r"(off));
+  return r;
+}
+__device__ __forceinline__ uint4 load_stream(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// A CTA's warps stand rw along the row blocks (R blocks each) and 8 / rw along
+// k, and the CTAs of a cluster split k further; partial sums meet in shared
+// memory, across the cluster through distributed shared memory.
+template <int NT, int R>
+__global__ void __launch_bounds__(kW4Threads) w4_kernel(const __grid_constant__ W4Args a) {
+  extern __shared__ float part[];  // [k warps][8 NT][rows + 4]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int S = cluster.num_blocks(), rank = cluster.block_rank();
+  const int kw = kW4Warps / a.rw, wr = warp % a.rw, wk = warp / a.rw;
+  const int cta_rows = 16 * R * a.rw, stride = cta_rows + 4;
+  const int rb0 = ((blockIdx.x / S) * a.rw + wr) * R;
+  const int p = rank * kw + wk, parts = S * kw;
+  const int k0 = (int)((long long)a.KT * p / parts), k1 = (int)((long long)a.KT * (p + 1) / parts);
+  const bool fine = a.group == 32;
+  const int tiles_per_group = a.group == 128 ? 2 : 1;
+
+  float acc[R][NT][4];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[r][nt][e] = 0.f;
+
+  constexpr int P = NT == 1 ? 4 : 2;  // tiles in flight
+  uint4 w[P][R];
+  uint2 sc[P][R];
+  auto fetch = [&](int i, int kt) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      w[i][r] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+      sc[i][r] = make_uint2(0u, 0u);
+      if (kt < k1 && rb0 + r < a.RB) {
+        w[i][r] = load_stream(a.codes + ((size_t)(rb0 + r) * a.KT + kt) * 32 + lane);
+        if (fine)
+          sc[i][r] = *(const uint2*)(a.scales + ((size_t)(rb0 + r) * a.sunits + kt) * 32 + 4 * g);
+        else
+          sc[i][r].x = *(const uint32_t*)(a.scales + ((size_t)(rb0 + r) * a.sunits + kt / tiles_per_group) * 16 + 2 * g);
+      }
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < P; ++i) fetch(i, k0 + i);
+  const uint16_t* xr = a.x + (int64_t)g * a.x_stride + 8 * t;
+  for (int kt = k0; kt < k1; kt += P) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      if (kt + i < k1) {
+        uint4 b[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            b[nt][h] = make_uint4(0u, 0u, 0u, 0u);
+            const int k = (kt + i) * kW4K + 32 * h;
+            if (nt * 8 + g < a.M && k < a.K) b[nt][h] = *(const uint4*)(xr + (int64_t)nt * 8 * a.x_stride + k);
+          }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const uint32_t words[4] = {w[i][r].x, w[i][r].y, w[i][r].z, w[i][r].w};
+          float s[2][2];  // [row half][32-k half]
+          if (fine) {
+            s[0][0] = bf2f(sc[i][r].x & 0xffffu);
+            s[0][1] = __uint_as_float(sc[i][r].x & 0xffff0000u);
+            s[1][0] = bf2f(sc[i][r].y & 0xffffu);
+            s[1][1] = __uint_as_float(sc[i][r].y & 0xffff0000u);
+          } else {
+            s[0][0] = s[0][1] = bf2f(sc[i][r].x & 0xffffu);
+            s[1][0] = s[1][1] = __uint_as_float(sc[i][r].x & 0xffff0000u);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t av[2][4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) av[e][j] = widen4(words[2 * h + e] >> (4 * j));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float c[4] = {0.f, 0.f, 0.f, 0.f};
+              mma_bf16(c, av[0], b[nt][h].x, b[nt][h].y);
+              mma_bf16(c, av[1], b[nt][h].z, b[nt][h].w);
+              acc[r][nt][0] = fmaf(c[0], s[0][h], acc[r][nt][0]);
+              acc[r][nt][1] = fmaf(c[1], s[0][h], acc[r][nt][1]);
+              acc[r][nt][2] = fmaf(c[2], s[1][h], acc[r][nt][2]);
+              acc[r][nt][3] = fmaf(c[3], s[1][h], acc[r][nt][3]);
+            }
+          }
+        }
+        fetch(i, kt + i + P);
+      }
+    }
+  }
+
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        part[(wk * 8 * NT + nt * 8 + 2 * t + (e & 1)) * stride + (wr * R + r) * 16 + g + 8 * (e >> 1)] = acc[r][nt][e];
+  if (S > 1) cluster.sync();
+  else __syncthreads();
+  const int n0 = (blockIdx.x / S) * cta_rows;
+  for (int idx = rank * kW4Threads + threadIdx.x; idx < cta_rows * a.M; idx += S * kW4Threads) {
+    const int m = idx / cta_rows, n = idx % cta_rows;
+    float v = 0.f;
+    for (int c = 0; c < S; ++c) {
+      const float* src = S > 1 ? cluster.map_shared_rank(part, c) : part;
+      for (int k = 0; k < kw; ++k) v += src[(k * 8 * NT + m) * stride + n];
+    }
+    if (n0 + n < a.N) {
+      if (a.y_f32) ((float*)a.y)[(int64_t)m * a.y_stride + n0 + n] = v;
+      else ((uint16_t*)a.y)[(int64_t)m * a.y_stride + n0 + n] = f2bf(v);
+    }
+  }
+  if (S > 1) cluster.sync();  // no CTA leaves while another reads its sums
+}
+
+// partial sums of the widest form: rw = 4, 2 k warps
+cudaError_t w4_setup() {
+  return cudaFuncSetAttribute(w4_kernel<8, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * 64 * (128 + 4) * 4);
+}
+
+template <int NT, int R>
+cudaError_t w4_launch(const W4Args& a, int S, cudaStream_t s) {
+  const int kw = kW4Warps / a.rw, cta_rows = 16 * R * a.rw;
+  cudaLaunchConfig_t lc{};
+  lc.gridDim = dim3((a.N + cta_rows - 1) / cta_rows * S);
+  lc.blockDim = dim3(kW4Threads);
+  lc.dynamicSmemBytes = (size_t)kw * 8 * NT * (cta_rows + 4) * sizeof(float);
+  lc.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = S;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  lc.attrs = at;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, w4_kernel<NT, R>, a);
+}
+
+char g_w4_err[256];
+
+int fail(qtts_w4* w, int code, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(w ? w->err : g_w4_err, 256, fmt, ap);
+  va_end(ap);
+  return code;
+}
+
+struct DeviceGuard {  // the caller's current device is put back on every path out
+  int prev = -1, dev;
+  bool ok;
+  explicit DeviceGuard(int d) : dev(d) {
+    if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
+    ok = prev == d || cudaSetDevice(d) == cudaSuccess;
+  }
+  ~DeviceGuard() {
+    if (prev >= 0 && prev != dev) cudaSetDevice(prev);
+  }
+};
+
+struct DeviceBuf {
+  void* p = nullptr;
+  cudaError_t alloc(size_t n) { return cudaMalloc(&p, n); }
+  ~DeviceBuf() {
+    if (p) cudaFree(p);
+  }
+};
+
+}  // namespace
+}  // namespace qtts
+
+using namespace qtts;
+
+extern "C" {
+
+const char* qtts_w4_last_error(const qtts_w4* w) { return w ? w->err : g_w4_err; }
+
+int qtts_w4_create(int N, int K, int group, int device, qtts_w4** out) {
+  if (!out) return fail(nullptr, QTTS_E_INVALID, "null argument");
+  *out = nullptr;
+  if (N < 1 || K < 1) return fail(nullptr, QTTS_E_INVALID, "N and K must be positive");
+  if (group != 32 && group != 64 && group != 128) return fail(nullptr, QTTS_E_INVALID, "group must be 32, 64 or 128");
+  if (K % group) return fail(nullptr, QTTS_E_INVALID, "K must be a multiple of the group");
+  if (N > (1 << 24) || K > (1 << 20)) return fail(nullptr, QTTS_E_INVALID, "N must be at most 2^24 and K at most 2^20");
+  int ndev = 0;
+  if (cudaGetDeviceCount(&ndev) != cudaSuccess || device < 0 || device >= ndev)
+    return fail(nullptr, QTTS_E_CUDA, "no CUDA device %d", device);
+  DeviceGuard g(device);
+  if (!g.ok) return fail(nullptr, QTTS_E_CUDA, "cudaSetDevice(%d) failed", device);
+  qtts_w4* w = new (std::nothrow) qtts_w4();
+  if (!w) return fail(nullptr, QTTS_E_OOM, "out of host memory");
+  w->N = N;
+  w->K = K;
+  w->group = group;
+  w->device = device;
+  w->RB = (N + kW4Rows - 1) / kW4Rows;
+  w->KT = (K + kW4K - 1) / kW4K;
+  const size_t ns = (size_t)w->RB * scale_units(w->KT, K, group) * (group == 32 ? 32 : 16);
+  cudaError_t e = cudaDeviceGetAttribute(&w->G, cudaDevAttrMultiProcessorCount, device);
+  if (e == cudaSuccess) e = w4_setup();
+  if (e == cudaSuccess) e = cudaMalloc((void**)&w->codes, (size_t)w->RB * w->KT * 512);
+  if (e == cudaSuccess) e = cudaMalloc((void**)&w->scales, ns * sizeof(uint16_t));
+  if (e == cudaSuccess) e = cudaMemset(w->scales, 0, ns * sizeof(uint16_t));
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    fail(nullptr, QTTS_E_OOM, "device allocation: %s", cudaGetErrorString(e));
+    qtts_w4_destroy(w);
+    return QTTS_E_OOM;
+  }
+  *out = w;
+  return QTTS_OK;
+}
+
+void qtts_w4_destroy(qtts_w4* w) {
+  if (!w) return;
+  {
+    DeviceGuard g(w->device);
+    if (w->codes) cudaFree(w->codes);
+    if (w->scales) cudaFree(w->scales);
+  }
+  delete w;
+}
+
+static int w4_fill(qtts_w4* w, const void* src, size_t src_bytes, const void* scales, const char* who) {
+  DeviceGuard g(w->device);
+  if (!g.ok) return fail(w, QTTS_E_CUDA, "cudaSetDevice failed");
+  const size_t nk = (size_t)w->N * w->K, ns = nk / w->group;
+  DeviceBuf in, q, s, bad;
+  cudaError_t e = in.alloc(src_bytes);
+  if (e == cudaSuccess && !scales) e = q.alloc(nk);
+  if (e == cudaSuccess) e = s.alloc(ns * sizeof(uint16_t));
+  if (e == cudaSuccess) e = bad.alloc(sizeof(int));
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail(w, QTTS_E_OOM, "%s: %s", who, cudaGetErrorString(e));
+  }
+  const int grid = 8 * w->G;
+  int flag = 0;
+  w->loaded = false;
+  // device sources may still be being written on the caller's streams
+  e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = cudaMemcpy(in.p, src, src_bytes, cudaMemcpyDefault);
+  if (e == cudaSuccess && scales) e = cudaMemcpy(s.p, scales, ns * sizeof(uint16_t), cudaMemcpyDefault);
+  if (e == cudaSuccess) e = cudaMemset(bad.p, 0, sizeof(int));
+  if (e == cudaSuccess && !scales) {
+    w4_quantize_kernel<<<grid, 256>>>((const uint16_t*)in.p, w->N, w->K, w->group, (int8_t*)q.p, (uint16_t*)s.p);
+    e = cudaGetLastError();
+  }
+  if (e == cudaSuccess) {
+    w4_pack_kernel<<<grid, 256>>>((const int8_t*)(scales ? in.p : q.p), (const uint16_t*)s.p, w->N, w->K, w->group,
+                                  w->RB, w->KT, w->codes, w->scales, (int*)bad.p);
+    e = cudaGetLastError();
+  }
+  if (e == cudaSuccess) e = cudaMemcpy(&flag, bad.p, sizeof(int), cudaMemcpyDeviceToHost);
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();
+  if (e != cudaSuccess) return fail(w, QTTS_E_CUDA, "%s: %s", who, cudaGetErrorString(e));
+  if (flag) return fail(w, QTTS_E_INVALID, "%s: a code outside -8..7", who);
+  w->loaded = true;
+  return QTTS_OK;
+}
+
+int qtts_w4_quantize(qtts_w4* w, const uint16_t* weights) {
+  if (!w) return QTTS_E_INVALID;
+  if (!weights) return fail(w, QTTS_E_INVALID, "qtts_w4_quantize: null argument");
+  return w4_fill(w, weights, (size_t)w->N * w->K * 2, nullptr, "qtts_w4_quantize");
+}
+
+int qtts_w4_load(qtts_w4* w, const int8_t* codes, const uint16_t* scales) {
+  if (!w) return QTTS_E_INVALID;
+  if (!codes || !scales) return fail(w, QTTS_E_INVALID, "qtts_w4_load: null argument");
+  return w4_fill(w, codes, (size_t)w->N * w->K, scales, "qtts_w4_load");
+}
+
+int qtts_w4_export(qtts_w4* w, int8_t* codes_host, uint16_t* scales_host) {
+  if (!w) return QTTS_E_INVALID;
+  if (!codes_host || !scales_host) return fail(w, QTTS_E_INVALID, "qtts_w4_export: null argument");
+  if (!w->loaded) return fail(w, QTTS_E_STATE, "qtts_w4_export: no weights loaded");
+  DeviceGuard g(w->device);
+  if (!g.ok) return fail(w, QTTS_E_CUDA, "cudaSetDevice failed");
+  const size_t nk = (size_t)w->N * w->K, ns = nk / w->group;
+  DeviceBuf q, s;
+  cudaError_t e = q.alloc(nk);
+  if (e == cudaSuccess) e = s.alloc(ns * sizeof(uint16_t));
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail(w, QTTS_E_OOM, "qtts_w4_export: %s", cudaGetErrorString(e));
+  }
+  w4_unpack_kernel<<<8 * w->G, 256>>>(w->codes, w->scales, w->N, w->K, w->group, w->KT, (int8_t*)q.p, (uint16_t*)s.p);
+  e = cudaGetLastError();
+  if (e == cudaSuccess) e = cudaMemcpy(codes_host, q.p, nk, cudaMemcpyDeviceToHost);
+  if (e == cudaSuccess) e = cudaMemcpy(scales_host, s.p, ns * sizeof(uint16_t), cudaMemcpyDeviceToHost);
+  if (e != cudaSuccess) return fail(w, QTTS_E_CUDA, "qtts_w4_export: %s", cudaGetErrorString(e));
+  return QTTS_OK;
+}
+
+int qtts_w4_linear(qtts_w4* w, int M, const uint16_t* x, int64_t x_stride, void* y, int64_t y_stride, int y_dtype,
+                   void* stream) {
+  if (!w) return QTTS_E_INVALID;
+  if (M < 0 || M > kW4MaxM) return fail(w, QTTS_E_BATCH, "qtts_w4_linear: M = %d outside 0..%d", M, kW4MaxM);
+  if (!w->loaded) return fail(w, QTTS_E_STATE, "qtts_w4_linear: no weights loaded");
+  if (y_dtype != QTTS_DTYPE_BF16 && y_dtype != QTTS_DTYPE_F32)
+    return fail(w, QTTS_E_INVALID, "qtts_w4_linear: y must be bf16 or fp32");
+  if (M == 0) return QTTS_OK;
+  if (!x || !y) return fail(w, QTTS_E_INVALID, "qtts_w4_linear: null argument");
+  if (((uintptr_t)x & 15) || x_stride < w->K || x_stride % 8)
+    return fail(w, QTTS_E_INVALID,
+                "qtts_w4_linear: x must be 16-byte aligned, with a row stride that is a multiple of 8 and holds a row");
+  if (((uintptr_t)y & (y_dtype == QTTS_DTYPE_F32 ? 3 : 1)) || y_stride < w->N)
+    return fail(w, QTTS_E_INVALID, "qtts_w4_linear: y must be aligned to its type, with a row stride that holds a row");
+  DeviceGuard g(w->device);
+  if (!g.ok) return fail(w, QTTS_E_CUDA, "cudaSetDevice failed");
+  W4Args a{w->codes, w->scales, w->N, w->K, w->RB, w->KT, w->group, scale_units(w->KT, w->K, w->group),
+           M, x, x_stride, y, y_stride, y_dtype == QTTS_DTYPE_F32, 1};
+  cudaError_t e;
+  const cudaStream_t s = (cudaStream_t)stream;
+  int S = 1;
+  if (M <= 8) {
+    while (S < 8 && w->RB * S < w->G && w->KT >= 2 * S * 2 * kW4Warps) S *= 2;
+    e = w4_launch<1, 1>(a, S, s);
+  } else {
+    a.rw = 4;
+    const int ctas = (w->RB + 7) / 8;
+    while (S < 8 && ctas * S < w->G && w->KT >= 2 * S * 2 * 2) S *= 2;
+    e = M <= 16 ? w4_launch<2, 2>(a, S, s) : M <= 32 ? w4_launch<4, 2>(a, S, s) : w4_launch<8, 2>(a, S, s);
+  }
+  if (e != cudaSuccess) return fail(w, QTTS_E_CUDA, "qtts_w4_linear: %s", cudaGetErrorString(e));
+  return QTTS_OK;
+}
+
+}  // extern "C"

@@ -116,6 +116,13 @@ SIGNATURES = [
                                                                        C.c_int64, _P, _P]),
     ("qtts_kv8_read", C.c_int, [_P] + [C.c_int] * 4 + [_P] * 3 + [C.c_int, _P, _P, _P]),
     ("qtts_kv8_status", C.c_int, [_P, C.POINTER(C.c_int)]),
+    ("qtts_w4_last_error", C.c_char_p, [_P]),
+    ("qtts_w4_create", C.c_int, [C.c_int] * 4 + [C.POINTER(_P)]),
+    ("qtts_w4_destroy", None, [_P]),
+    ("qtts_w4_quantize", C.c_int, [_P, _P]),
+    ("qtts_w4_load", C.c_int, [_P, _P, _P]),
+    ("qtts_w4_export", C.c_int, [_P, _P, _P]),
+    ("qtts_w4_linear", C.c_int, [_P, C.c_int, _P, C.c_int64, _P, C.c_int64, C.c_int, _P]),
 ]
 
 
@@ -363,3 +370,37 @@ def qtts_kv8_status(c, raise_on_error=True):
     if raise_on_error:
         _check_kv8(c, rc)
     return rc, e.value
+
+
+def _check_w4(w, rc):
+    if rc != QTTS_OK:
+        raise QttsError(rc, load_library().qtts_w4_last_error(w).decode())
+    return rc
+
+
+def qtts_w4_create(N, K, group, device=0):
+    w = C.c_void_p()
+    _check_w4(None, load_library().qtts_w4_create(N, K, group, device, C.byref(w)))
+    return w
+
+
+def qtts_w4_destroy(w):
+    load_library().qtts_w4_destroy(w)
+
+
+def qtts_w4_quantize(w, weights):
+    """weights: bf16 bits [N][K], host or device."""
+    return _check_w4(w, load_library().qtts_w4_quantize(w, ptr(weights)))
+
+
+def qtts_w4_load(w, codes, scales):
+    return _check_w4(w, load_library().qtts_w4_load(w, ptr(codes), ptr(scales)))
+
+
+def qtts_w4_export(w, codes_host, scales_host):
+    return _check_w4(w, load_library().qtts_w4_export(w, ptr(codes_host), ptr(scales_host)))
+
+
+def qtts_w4_linear(w, M, x, x_stride, y, y_stride, y_dtype, stream=None):
+    return _check_w4(w, load_library().qtts_w4_linear(w, M, ptr(x), x_stride, ptr(y), y_stride, y_dtype,
+                                                      _stream(stream)))

@@ -481,6 +481,39 @@ int qtts_kv8_read(qtts_kv8* c, int layer, int B, int n_rows, int max_new, const 
  * (QTTS_DEV_*). Returns QTTS_E_DEVICE / QTTS_E_TIMEOUT when it was set. */
 int qtts_kv8_status(qtts_kv8* c, int* device_err);
 
+/* ---------------------------------------------------------------------------
+ * Products with 4-bit weights: a linear layer's [N][K] matrix held as codes of
+ * 4 bits with one bf16 scale for each row and group of 32, 64 or 128
+ * consecutive k, for up to 64 activation rows (a decode step's). A quarter of
+ * the bf16 weights' bytes, half of qtts_quantize_int8's.
+ * ------------------------------------------------------------------------- */
+typedef struct qtts_w4 qtts_w4;
+
+const char* qtts_w4_last_error(const qtts_w4* w); /* w may be NULL for create errors */
+/* N 1..2^24 rows (any number), K 1..2^20, a multiple of group. */
+int qtts_w4_create(int N, int K, int group, int device, qtts_w4** out);
+void qtts_w4_destroy(qtts_w4* w);
+
+/* Quantise bf16 weights [N][K] (host or device): scale = bf16(max|w| / 7) of
+ * the row's group, code = round-half-even(w / scale) clamped to [-7, 7], in
+ * binary32; a scale below the normal numbers is 0 with its codes 0, a group
+ * with a NaN or an infinity gets a NaN scale. Synchronous. */
+int qtts_w4_quantize(qtts_w4* w, const uint16_t* weights);
+/* Take codes [N][K] in -8..7 and bf16 scales [N][K / group] as they are (host
+ * or device). Synchronous. */
+int qtts_w4_load(qtts_w4* w, const int8_t* codes, const uint16_t* scales);
+/* Copy codes [N][K] and bf16 scales [N][K / group] to host memory. */
+int qtts_w4_export(qtts_w4* w, int8_t* codes_host, uint16_t* scales_host);
+
+/* y[m][n] = sum_k x[m][k] * code[n][k] * scale[n][k / group], summed in fp32,
+ * for m = 0..M - 1, M at most 64 (0: nothing). x: device bf16 [M][K], 16-byte
+ * aligned, x_stride elements between rows (a multiple of 8); y: device
+ * [M][N], bf16 (QTTS_DTYPE_BF16, rounded once) or fp32 (QTTS_DTYPE_F32),
+ * y_stride elements between rows. x and y must not overlap. Asynchronous on
+ * `stream`, allocates nothing, can be captured into a graph. */
+int qtts_w4_linear(qtts_w4* w, int M, const uint16_t* x, int64_t x_stride, void* y, int64_t y_stride, int y_dtype,
+                   void* stream);
+
 #ifdef __cplusplus
 }
 #endif
