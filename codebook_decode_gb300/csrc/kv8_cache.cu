@@ -13,7 +13,9 @@
 namespace qtts {
 namespace {
 
-constexpr int kWarpsPerCta = 4;  // one warp per (page, head, K or V) block
+// One warp per (page, head, K or V) block; a CTA takes up to 16 blocks of one
+// page of one session.
+constexpr int kMaxWarps = 16;
 
 // The rotation table: angles in double (a position of a long context times a
 // frequency loses its fraction in fp32), stored fp32.
@@ -32,118 +34,163 @@ __device__ __forceinline__ float4 bf4(uint2 v) {
   return make_float4(bf2f(v.x & 0xffffu), __uint_as_float(v.x & 0xffff0000u), bf2f(v.y & 0xffffu),
                      __uint_as_float(v.y & 0xffff0000u));
 }
-__device__ __forceinline__ uint32_t abs_bits4(float4 v) {
-  const uint32_t m = 0x7fffffffu;
-  return max(max(__float_as_uint(v.x) & m, __float_as_uint(v.y) & m),
-             max(__float_as_uint(v.z) & m, __float_as_uint(v.w) & m));
+// largest magnitude of the three, NaN if one is
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
-__device__ __forceinline__ uint32_t code(float x, float inv) {
-  return (uint32_t)(__float2int_rn(fminf(fmaxf(x * inv, -127.f), 127.f)) + 128);
+// Rounding to an integer by adding 1.5 * 2^23 (half-even, like the product
+// before it in binary32); with 128 on top the low byte is the stored code. No
+// clamp: x * inv is at most 127 (1 + 2^-22).
+__device__ __forceinline__ uint32_t code_bits(float x, float inv) {
+  return __float_as_uint(__fadd_rn(__fmul_rn(x, inv), 12583040.f));
 }
-__device__ __forceinline__ uint32_t codes4(float4 v, float inv) {
-  return code(v.x, inv) | code(v.y, inv) << 8 | code(v.z, inv) << 16 | code(v.w, inv) << 24;
+__device__ __forceinline__ uint32_t codes4(float x, float y, float z, float w, float inv) {
+  return __byte_perm(__byte_perm(code_bits(x, inv), code_bits(y, inv), 0x0040),
+                     __byte_perm(code_bits(z, inv), code_bits(w, inv), 0x0040), 0x5410);
+}
+// byte i of c as its code: the byte under the exponent of 2^23, minus 2^23 + 128
+__device__ __forceinline__ float code_value(uint32_t c, int i) {
+  return __uint_as_float(__byte_perm(c, 0x4b000000u, 0x7550 | i)) - 8388736.f;
 }
 // codes at scale s_old as codes at a larger scale, r = s_old / s
 __device__ __forceinline__ uint32_t rescale4(uint32_t c, float r) {
-  uint32_t o = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o |= code((float)((int)(c >> (8 * i) & 255u) - 128), r) << (8 * i);
-  return o;
+  return codes4(code_value(c, 0), code_value(c, 1), code_value(c, 2), code_value(c, 3), r);
 }
 
-struct BlockTask {
-  int b, page, h, which;  // which: 0 K, 1 V
-  int first, last;        // slots [first, last) of the page take new rows
-  int pos0, row0;         // position and packed row of slot `first`
+// The page that a CTA works on and its new rows; valid: there are any.
+struct PageTask {
+  int page_index;
+  int first, last;  // slots [first, last) of the page take new rows
+  int pos0, row0;   // position and packed row of slot `first`
+  bool valid;
 };
-// The block that this warp works on; false: none, or a page outside the pool.
-__device__ __forceinline__ bool block_task(const Kv8View& c, const Kv8Batch& q, int touched, BlockTask* t) {
-  t->b = blockIdx.x / touched;
-  const int k = blockIdx.x % touched;
-  const int task = blockIdx.y * kWarpsPerCta + threadIdx.x / 32;
-  if (task >= 2 * c.nkv) return false;
-  t->h = task >> 1;
-  t->which = task & 1;
-  const Kv8Session s = kv8_session(q, t->b, c.max_context, c.err);
-  if (s.n == 0) return false;
-  const int pi = s.L / kPage + k;
-  const int lo = max(s.L, pi * kPage), hi = min(s.L + s.n, (pi + 1) * kPage);
-  if (lo >= hi) return false;
-  t->page = q.bt[(size_t)t->b * q.bt_stride + pi];
-  if (t->page < 0 || t->page >= c.pool_pages) {
-    set_err(c.err, QTTS_DEV_BAD_PAGE);
-    return false;
-  }
-  t->first = lo - pi * kPage;
-  t->last = hi - pi * kPage;
-  t->pos0 = lo;
-  t->row0 = s.r0 + lo - s.L;
-  return true;
+__device__ __forceinline__ PageTask page_task(const Kv8View& c, const Kv8Batch& q, int b, int k) {
+  PageTask t;
+  const Kv8Session s = kv8_session(q, b, c.max_context, c.err);
+  t.page_index = s.L / kPage + k;
+  const int lo = max(s.L, t.page_index * kPage), hi = min(s.L + s.n, (t.page_index + 1) * kPage);
+  t.valid = s.n > 0 && lo < hi;
+  t.first = lo - t.page_index * kPage;
+  t.last = hi - t.page_index * kPage;
+  t.pos0 = lo;
+  t.row0 = s.r0 + lo - s.L;
+  return t;
+}
+// The page's id, or -1 with the error word set.
+__device__ __forceinline__ int page_id(const Kv8View& c, const Kv8Batch& q, int b, int page_index) {
+  const int page = q.bt[(size_t)b * q.bt_stride + page_index];
+  if (page >= 0 && page < c.pool_pages) return page;
+  set_err(c.err, QTTS_DEV_BAD_PAGE);
+  return -1;
+}
+
+// A block's new scale, from its new values' largest magnitude (as bits).
+__device__ __forceinline__ float new_scale(uint32_t amax, float s_old) {
+  float s = __uint_as_float(amax) / 127.f;
+  if (s < kKv8MinScale) s = 0.f;
+  if (amax >= 0x7f800000u || s_old != s_old) s = __int_as_float(0x7fffffff);
+  return s_old > s ? s_old : s;
 }
 
 // Append: one warp per block, everything it adds to the block in registers:
 // read the rows once, rotate (K), take the block's largest magnitude, quantise,
-// write. Rows are read 8 bytes a lane (a token's head is 256 contiguous bytes
-// at d = 128). Bound by bytes for prompts and by latency for single tokens.
+// write. Bound by bytes for prompts and by latency for single tokens, so the
+// rows are asked for as soon as the session's lengths are there, together with
+// the page's id and the rotation (once per CTA, in shared memory).
 template <int D>
-__global__ void __launch_bounds__(kWarpsPerCta * 32)
+__global__ void __launch_bounds__(kMaxWarps * 32, 2)
     append_kernel(Kv8View c, Kv8Batch q, int touched, const uint16_t* __restrict__ k, int64_t k_stride,
                   const uint16_t* __restrict__ v, int64_t v_stride) {
-  BlockTask t;
-  if (!block_task(c, q, touched, &t)) return;
-  const int lane = threadIdx.x & 31;
-  const size_t blk = (size_t)t.page * c.nkv + t.h;
-  uint8_t* codes = c.codes + blk * (32 * D) + t.which * (16 * D);
-  float* sp = c.scales + blk * 2 + t.which;
+  __shared__ __align__(16) float cs[kPage][D / 2], sn[kPage][D / 2];
+  const int b = blockIdx.x / touched;
+  const PageTask t = page_task(c, q, b, blockIdx.x % touched);
+  if (!t.valid) return;
+  const int lane = threadIdx.x & 31, task = blockIdx.y * (blockDim.x / 32) + threadIdx.x / 32;
+  const bool active = task < 2 * c.nkv;
+  const int h = task >> 1, which = task & 1;  // K, V
+
+  // K: lanes of a token take dims 4i..4i+3 and their rotation partners d/2
+  // further. V: a lane takes 4 dims of the tokens of NQ quads. 16 words either way
+  constexpr int LPT = D / 8, TPP = 32 / LPT, PASSES = kPage / TPP;
+  constexpr int NQ = D / 32, WORDS = 4 * NQ;
+  static_assert(2 * PASSES == WORDS, "K and V words of a lane");
+  const int i4 = lane % LPT * 4, tk = lane / LPT;                    // K
+  const int x4 = lane % (D / 4), t0 = lane / (D / 4) * NQ;           // V
+  auto v_slot = [&](int n, int j) { return 2 * (t0 + n) + (j & 1) + (j >> 1) * 8; };
+  const bool all = t.first == 0 && t.last == kPage;
+  auto fresh_slot = [&](int slot) { return all || (slot >= t.first && slot < t.last); };
+  uint2 raw[WORDS];
+  if (active && which == 0) {
+    const uint16_t* src = k + (int64_t)(t.row0 - t.first + tk) * k_stride + h * D + i4;
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p, src += TPP * k_stride) {
+      raw[2 * p] = raw[2 * p + 1] = make_uint2(0u, 0u);
+      if (fresh_slot(p * TPP + tk)) {
+        raw[2 * p] = __ldcs((const uint2*)src);
+        raw[2 * p + 1] = __ldcs((const uint2*)(src + D / 2));
+      }
+    }
+  } else if (active) {
+    const uint16_t* src = v + (int64_t)(t.row0 - t.first + 2 * t0) * v_stride + h * D + x4 * 4;
+#pragma unroll
+    for (int n = 0; n < NQ; ++n, src += 2 * v_stride)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        raw[4 * n + j] = make_uint2(0u, 0u);
+        if (fresh_slot(v_slot(n, j))) raw[4 * n + j] = __ldcs((const uint2*)(src + ((j & 1) + (j >> 1) * 8) * v_stride));
+      }
+  }
+  const int page = page_id(c, q, b, t.page_index);
+  if (c.rope_cos) {
+    const int n4 = (t.last - t.first) * (D / 8);  // float4s of each table
+    const float4* c4 = (const float4*)(c.rope_cos + (size_t)t.pos0 * (D / 2));
+    const float4* s4 = (const float4*)(c.rope_sin + (size_t)t.pos0 * (D / 2));
+    for (int i = threadIdx.x; i < n4; i += blockDim.x) {
+      ((float4*)cs[t.first])[i] = c4[i];
+      ((float4*)sn[t.first])[i] = s4[i];
+    }
+    __syncthreads();
+  }
+  if (!active || page < 0) return;
+
+  const size_t blk = (size_t)page * c.nkv + h;
+  uint8_t* codes = c.codes + blk * (32 * D) + which * (16 * D);
+  float* sp = c.scales + blk * 2 + which;
   // the tokens before the first new slot stay; their scale counts
   const float s_old = t.first > 0 ? *sp : 0.f;
-  uint32_t amax = 0;
 
-  if (t.which == 0) {
-    // lanes of a token take dims 4i..4i+3 and their rotation partners d/2 further
-    constexpr int LPT = D / 8, TPP = 32 / LPT, PASSES = kPage / TPP;
-    const int i4 = lane % LPT * 4, tk = lane / LPT;
-    float4 a[PASSES], b[PASSES];
+  if (which == 0) {
+    float4 a[PASSES], p4[PASSES];
+    float mx = 0.f;
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
       const int slot = p * TPP + tk;
-      a[p] = b[p] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (slot >= t.first && slot < t.last) {
-        const uint16_t* row = k + (int64_t)(t.row0 + slot - t.first) * k_stride + t.h * D + i4;
-        a[p] = bf4(*(const uint2*)row);
-        b[p] = bf4(*(const uint2*)(row + D / 2));
+      float4 x = bf4(raw[2 * p]), y = bf4(raw[2 * p + 1]);
+      if (c.rope_cos && fresh_slot(slot)) {
+        const float4 f = *(const float4*)&cs[slot][i4], g = *(const float4*)&sn[slot][i4];
+        const float4 u = x, w = y;
+        x = make_float4(u.x * f.x - w.x * g.x, u.y * f.y - w.y * g.y, u.z * f.z - w.z * g.z, u.w * f.w - w.w * g.w);
+        y = make_float4(w.x * f.x + u.x * g.x, w.y * f.y + u.y * g.y, w.z * f.z + u.z * g.z, w.w * f.w + u.w * g.w);
       }
+      a[p] = x;
+      p4[p] = y;
+      mx = max_abs(max_abs(mx, x.x, x.y), x.z, x.w);
+      mx = max_abs(max_abs(mx, y.x, y.y), y.z, y.w);
     }
-#pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-      const int slot = p * TPP + tk;
-      if (c.rope_cos && slot >= t.first && slot < t.last) {
-        const size_t at = (size_t)(t.pos0 + slot - t.first) * (D / 2) + i4;
-        const float4 cs = *(const float4*)(c.rope_cos + at), sn = *(const float4*)(c.rope_sin + at);
-        const float4 x = a[p], y = b[p];
-        a[p] = make_float4(x.x * cs.x - y.x * sn.x, x.y * cs.y - y.y * sn.y, x.z * cs.z - y.z * sn.z,
-                           x.w * cs.w - y.w * sn.w);
-        b[p] = make_float4(y.x * cs.x + x.x * sn.x, y.y * cs.y + x.y * sn.y, y.z * cs.z + x.z * sn.z,
-                           y.w * cs.w + x.w * sn.w);
-      }
-      amax = max(amax, max(abs_bits4(a[p]), abs_bits4(b[p])));
-    }
-    amax = __reduce_max_sync(0xffffffffu, amax);
-    float s = __uint_as_float(amax) / 127.f;
-    if (s < kKv8MinScale) s = 0.f;
-    if (amax >= 0x7f800000u || s_old != s_old) s = __int_as_float(0x7fffffff);
-    if (s_old > s) s = s_old;
+    const float s = new_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)), s_old);
     const float inv = s > 0.f ? 1.f / s : 0.f;
-    // dims x of token `slot` stand at [x / 64][slot][x % 64]
-    auto at = [&](int slot, int x) { return (uint32_t*)(codes + x / 64 * 1024 + slot * 64 + x % 64); };
     const bool grown = s > s_old && s_old > 0.f;
     const float r = grown ? s_old / s : 0.f;
+    // dims x of token `slot` stand at [x / 64][slot][x % 64]
+    auto at = [&](int slot, int x) { return (uint32_t*)(codes + x / 64 * 1024 + slot * 64 + x % 64); };
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
       const int slot = p * TPP + tk;
-      if (slot >= t.first && slot < t.last) {
-        *at(slot, i4) = codes4(a[p], inv);
-        *at(slot, i4 + D / 2) = codes4(b[p], inv);
+      if (fresh_slot(slot)) {
+        *at(slot, i4) = codes4(a[p].x, a[p].y, a[p].z, a[p].w, inv);
+        *at(slot, i4 + D / 2) = codes4(p4[p].x, p4[p].y, p4[p].z, p4[p].w, inv);
       } else if (grown && slot < t.first) {
         *at(slot, i4) = rescale4(*at(slot, i4), r);
         *at(slot, i4 + D / 2) = rescale4(*at(slot, i4 + D / 2), r);
@@ -152,94 +199,89 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32)
     __syncwarp();  // every lane has read the old scale
     if (lane == 0) *sp = s;
   } else {
-    // a lane takes 4 dims of the tokens of NQ quads: 16-byte words of 4 dims x 4 tokens
-    constexpr int NQ = D / 32;
-    const int x4 = lane % (D / 4), t0 = lane / (D / 4) * NQ;
-    float4 a[NQ][4];
+    uint32_t mx = 0;  // two magnitudes as 16-bit halves
 #pragma unroll
-    for (int n = 0; n < NQ; ++n)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int slot = 2 * (t0 + n) + (j & 1) + (j >> 1) * 8;
-        a[n][j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (slot >= t.first && slot < t.last)
-          a[n][j] = bf4(*(const uint2*)(v + (int64_t)(t.row0 + slot - t.first) * v_stride + t.h * D + x4 * 4));
-        amax = max(amax, abs_bits4(a[n][j]));
-      }
-    amax = __reduce_max_sync(0xffffffffu, amax);
-    float s = __uint_as_float(amax) / 127.f;
-    if (s < kKv8MinScale) s = 0.f;
-    if (amax >= 0x7f800000u || s_old != s_old) s = __int_as_float(0x7fffffff);
-    if (s_old > s) s = s_old;
+    for (int p = 0; p < WORDS; ++p) mx = __vmaxu2(mx, __vmaxu2(raw[p].x & 0x7fff7fffu, raw[p].y & 0x7fff7fffu));
+    mx = max(mx & 0xffffu, mx >> 16) << 16;
+    const float s = new_scale(__reduce_max_sync(0xffffffffu, mx), s_old);
     const float inv = s > 0.f ? 1.f / s : 0.f;
-    const bool whole = t.first == 0 && t.last == kPage;
     const bool grown = s > s_old && s_old > 0.f;
     const float r = grown ? s_old / s : 0.f;
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-      uint4* w = (uint4*)(codes + x4 * 64 + (t0 + n) * 16);
-      uint4 o = make_uint4(0, 0, 0, 0);
-      if (!whole) o = *w;
-      uint32_t* ow = &o.x;  // word i: dim 4 x4 + i, byte j: token j of the quad
+      uint4* dst = (uint4*)(codes + x4 * 64 + (t0 + n) * 16);
+      const float4 y0 = bf4(raw[4 * n]), y1 = bf4(raw[4 * n + 1]), y2 = bf4(raw[4 * n + 2]), y3 = bf4(raw[4 * n + 3]);
+      // word i: dim 4 x4 + i, byte j: token j of the quad
+      uint4 o = make_uint4(codes4(y0.x, y1.x, y2.x, y3.x, inv), codes4(y0.y, y1.y, y2.y, y3.y, inv),
+                           codes4(y0.z, y1.z, y2.z, y3.z, inv), codes4(y0.w, y1.w, y2.w, y3.w, inv));
+      if (!all) {
+        uint4 old = *dst;
+        uint32_t fresh = 0, before = 0;  // byte masks of the new tokens, of those before them
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int slot = 2 * (t0 + n) + (j & 1) + (j >> 1) * 8;
-        if (slot >= t.first && slot < t.last) {
-          const float* f = &a[n][j].x;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) ow[i] = (ow[i] & ~(255u << (8 * j))) | code(f[i], inv) << (8 * j);
-        } else if (grown && slot < t.first) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float old = (float)((int)(ow[i] >> (8 * j) & 255u) - 128);
-            ow[i] = (ow[i] & ~(255u << (8 * j))) | code(old, r) << (8 * j);
-          }
+        for (int j = 0; j < 4; ++j) {
+          if (v_slot(n, j) >= t.first && v_slot(n, j) < t.last) fresh |= 255u << (8 * j);
+          if (v_slot(n, j) < t.first) before |= 255u << (8 * j);
         }
+        if (!grown) before = 0;
+        auto merge = [&](uint32_t now, uint32_t was) {
+          if (before) was = (was & ~before) | (rescale4(was, r) & before);
+          return (now & fresh) | (was & ~fresh);
+        };
+        o = make_uint4(merge(o.x, old.x), merge(o.y, old.y), merge(o.z, old.z), merge(o.w, old.w));
       }
-      *w = o;
+      *dst = o;
     }
-    __syncwarp();  // every lane has read the old scale
+    __syncwarp();
     if (lane == 0) *sp = s;
   }
 }
 
 // Read-back: codes times scale as bf16, one warp per block, rows packed.
 template <int D>
-__global__ void __launch_bounds__(kWarpsPerCta * 32)
+__global__ void __launch_bounds__(kMaxWarps * 32, 4)
     read_kernel(Kv8View c, Kv8Batch q, int touched, uint16_t* __restrict__ k, uint16_t* __restrict__ v) {
-  BlockTask t;
-  if (!block_task(c, q, touched, &t)) return;
-  const int lane = threadIdx.x & 31;
-  const size_t blk = (size_t)t.page * c.nkv + t.h;
-  const uint8_t* codes = c.codes + blk * (32 * D) + t.which * (16 * D);
-  const float s = c.scales[blk * 2 + t.which];
-  auto val = [&](uint32_t byte) { return (uint32_t)f2bf((float)((int)(byte & 255u) - 128) * s); };
-  if (t.which == 0) {
-    constexpr int LPT = D / 4, TPP = 32 / LPT;
+  const int b = blockIdx.x / touched;
+  const PageTask t = page_task(c, q, b, blockIdx.x % touched);
+  const int lane = threadIdx.x & 31, task = blockIdx.y * (blockDim.x / 32) + threadIdx.x / 32;
+  if (!t.valid || task >= 2 * c.nkv) return;
+  const int h = task >> 1, which = task & 1;
+  const int page = page_id(c, q, b, t.page_index);
+  if (page < 0) return;
+  const size_t blk = (size_t)page * c.nkv + h;
+  const uint8_t* codes = c.codes + blk * (32 * D) + which * (16 * D);
+  const float s = c.scales[blk * 2 + which];
+  const bool all = t.first == 0 && t.last == kPage;
+  auto wanted = [&](int slot) { return all || (slot >= t.first && slot < t.last); };
+  const int64_t pitch = (int64_t)c.nkv * D;
+  auto pair = [&](uint32_t w0, int i0, uint32_t w1, int i1) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(code_value(w0, i0) * s, code_value(w1, i1) * s);
+    return *(const uint32_t*)&p;
+  };
+  if (which == 0) {
+    constexpr int LPT = D / 4, TPP = 32 / LPT, PASSES = kPage / TPP;
     const int x = lane % LPT * 4;
+    uint32_t w[PASSES];
 #pragma unroll
-    for (int p = 0; p < kPage / TPP; ++p) {
-      const int slot = p * TPP + lane / LPT;
-      if (slot < t.first || slot >= t.last) continue;
-      const uint32_t w = *(const uint32_t*)(codes + x / 64 * 1024 + slot * 64 + x % 64);
-      uint16_t* o = k + ((size_t)(t.row0 + slot - t.first) * c.nkv + t.h) * D + x;
-      *(uint2*)o = make_uint2(val(w) | val(w >> 8) << 16, val(w >> 16) | val(w >> 24) << 16);
-    }
+    for (int p = 0; p < PASSES; ++p) w[p] = *(const uint32_t*)(codes + x / 64 * 1024 + (p * TPP + lane / LPT) * 64 + x % 64);
+    uint16_t* o = k + (t.row0 - t.first + lane / LPT) * pitch + h * D + x;
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p, o += TPP * pitch)
+      if (wanted(p * TPP + lane / LPT))
+        __stcs((uint2*)o, make_uint2(pair(w[p], 0, w[p], 1), pair(w[p], 2, w[p], 3)));
   } else {
     constexpr int NQ = D / 32;
     const int x4 = lane % (D / 4), t0 = lane / (D / 4) * NQ;
+    uint4 w[NQ];
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      const uint4 w = *(const uint4*)(codes + x4 * 64 + (t0 + n) * 16);
+    for (int n = 0; n < NQ; ++n) w[n] = *(const uint4*)(codes + x4 * 64 + (t0 + n) * 16);
+    uint16_t* o = v + (t.row0 - t.first + 2 * t0) * pitch + h * D + x4 * 4;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int slot = 2 * (t0 + n) + (j & 1) + (j >> 1) * 8;
-        if (slot < t.first || slot >= t.last) continue;
-        uint16_t* o = v + ((size_t)(t.row0 + slot - t.first) * c.nkv + t.h) * D + x4 * 4;
-        *(uint2*)o = make_uint2(val(w.x >> (8 * j)) | val(w.y >> (8 * j)) << 16,
-                                val(w.z >> (8 * j)) | val(w.w >> (8 * j)) << 16);
-      }
-    }
+    for (int n = 0; n < NQ; ++n, o += 2 * pitch)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (wanted(2 * (t0 + n) + (j & 1) + (j >> 1) * 8))
+          __stcs((uint2*)(o + ((j & 1) + (j >> 1) * 8) * pitch),
+                 make_uint2(pair(w[n].x, j, w[n].y, j), pair(w[n].z, j, w[n].w, j)));
   }
 }
 
@@ -437,8 +479,9 @@ int qtts_kv8_append(qtts_kv8* c, int layer, int B, int n_rows, int max_new, cons
   if (!g.ok) return fail(c, QTTS_E_CUDA, "cudaSetDevice failed");
   const int touched = touched_pages(std::min(max_new, n_rows));
   if ((long long)B * touched > 0x7fffffffll) return fail(c, QTTS_E_INVALID, "qtts_kv8_append: too many rows");
-  const dim3 grid(B * touched, (2 * f.n_kv_heads + kWarpsPerCta - 1) / kWarpsPerCta);
-  const cudaError_t e = launch(f.head_dim == 64 ? append_kernel<64> : append_kernel<128>, grid, kWarpsPerCta * 32,
+  const int warps = std::min(2 * f.n_kv_heads, kMaxWarps);
+  const dim3 grid(B * touched, (2 * f.n_kv_heads + warps - 1) / warps);
+  const cudaError_t e = launch(f.head_dim == 64 ? append_kernel<64> : append_kernel<128>, grid, warps * 32,
                                (cudaStream_t)stream, view(c, layer), q, touched, k, k_stride, v, v_stride);
   if (e != cudaSuccess) return fail(c, QTTS_E_CUDA, "qtts_kv8_append: %s", cudaGetErrorString(e));
   return QTTS_OK;
@@ -460,8 +503,9 @@ int qtts_kv8_read(qtts_kv8* c, int layer, int B, int n_rows, int max_new, const 
   if (!g.ok) return fail(c, QTTS_E_CUDA, "cudaSetDevice failed");
   const int touched = touched_pages(std::min(max_new, n_rows));
   if ((long long)B * touched > 0x7fffffffll) return fail(c, QTTS_E_INVALID, "qtts_kv8_read: too many rows");
-  const dim3 grid(B * touched, (2 * f.n_kv_heads + kWarpsPerCta - 1) / kWarpsPerCta);
-  const cudaError_t e = launch(f.head_dim == 64 ? read_kernel<64> : read_kernel<128>, grid, kWarpsPerCta * 32,
+  const int warps = std::min(2 * f.n_kv_heads, kMaxWarps);
+  const dim3 grid(B * touched, (2 * f.n_kv_heads + warps - 1) / warps);
+  const cudaError_t e = launch(f.head_dim == 64 ? read_kernel<64> : read_kernel<128>, grid, warps * 32,
                                (cudaStream_t)stream, view(c, layer), q, touched, k_out, v_out);
   if (e != cudaSuccess) return fail(c, QTTS_E_CUDA, "qtts_kv8_read: %s", cudaGetErrorString(e));
   return QTTS_OK;
