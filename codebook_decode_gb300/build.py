@@ -14,7 +14,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libqtts.so")
 SOURCES = ["frame_kernel.cu", "util_kernels.cu", "qtts_api.cu", "kv_noalloc.cu", "prefill.cu",
-           "kv8_cache.cu", "kv8_attention.cu", "w4_linear.cu"]
+           "kv8_cache.cu", "kv8_attention.cu", "kv8_chunk.cu", "w4_linear.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
@@ -28,7 +28,8 @@ def _stale(obj, src):
     if not os.path.exists(obj):
         return True
     deps = [src, os.path.join(CSRC, "qtts_internal.h"), os.path.join(CSRC, "device_util.cuh"),
-            os.path.join(CSRC, "kv8.cuh"),            os.path.join(ROOT, "include", "qtts.h")]
+            os.path.join(CSRC, "kv8.cuh"), os.path.join(CSRC, "kv8_attn.cuh"),
+            os.path.join(ROOT, "include", "qtts.h")]
     return any(os.path.getmtime(d) > os.path.getmtime(obj) for d in deps)
 
 

@@ -93,6 +93,11 @@ __device__ __forceinline__ Kv8Session kv8_session(const Kv8Batch& q, int b, int 
   return s;
 }
 
+cudaError_t kv8_chunk_setup(int d);
+size_t kv8_chunk_workspace(int d, int sms);
+cudaError_t kv8_chunk(const Kv8View& v, const Kv8Batch& q, int d, int group, int sms, const uint16_t* qp,
+                      int64_t q_stride, float scale, uint16_t* out, int64_t out_stride, unsigned* arrived, float* part,
+                      cudaStream_t s);
 cudaError_t kv8_attention_setup(int d);
 size_t kv8_attention_workspace(int d, int sms);
 cudaError_t kv8_attention(const Kv8View& v, const Kv8Batch& q, int d, int group, int sms, const uint16_t* qp,

@@ -30,13 +30,11 @@
 #include <algorithm>
 
 #include "kv8.cuh"
+#include "kv8_attn.cuh"
 
 namespace qtts {
 namespace {
 
-constexpr float kSlack = 6.f;
-constexpr float kNone = -1.5e38f;  // running maximum before the first value
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kWaitTries = 1 << 20;  // bound of each wait for a copy (a try suspends for microseconds)
 constexpr int kMaxCols = 32;
 // A tile of up to this many pages goes to one CTA when there are enough CTAs
@@ -97,24 +95,6 @@ __device__ __forceinline__ bool wait_copy(uint64_t* bar, uint32_t parity) {
     if (mbar_test(bar, parity)) return true;
   return false;
 }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float lg2(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// Four codes to two half pairs: a byte under the exponent of 2^10 is 1024 +
-// byte, minus 1152 the code itself, exactly.
-__device__ __forceinline__ void widen(uint32_t c, uint32_t& lo, uint32_t& hi) {
-  const uint32_t a = __byte_perm(c, 0x64646464u, 0x4140), b = __byte_perm(c, 0x64646464u, 0x4342);
-  const uint32_t off = 0x64806480u;
-  asm("sub.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(off));
-  asm("sub.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(off));
-}
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -126,16 +106,11 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
-__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *(const uint32_t*)&h;
-}
-
 struct Args {
   Kv8View c;
   Kv8Batch q;
-  int group, rows_per_tile, max_cols;
-  bool one_tile;  // every session is one tile and every tile can have its CTA
+  int group, max_cols;
+  bool one_each;  // every tile can have its CTA
   const uint16_t* qp;
   int64_t q_stride;
   float scale_log2;
@@ -145,10 +120,8 @@ struct Args {
   unsigned* arrived;  // [CTAs] CTAs of the tile that starts in this CTA and ends in a later one; zero between calls
 };
 
-// pages that the last row of tile t sees
-__device__ __forceinline__ int tile_pages(int L, int n, int t, int rows_per_tile) {
-  return (L + min((t + 1) * rows_per_tile, n) + kPage - 1) / kPage;
-}
+// pages that a tile's last row sees
+__device__ __forceinline__ int tile_pages(int L, int n) { return (L + n + kPage - 1) / kPage; }
 
 // A part of a tile that one warp worked on: the tile's first unit, pages, first
 // packed row, kv head and columns (0: no piece), and whether it reaches its end.
@@ -156,36 +129,23 @@ struct Piece {
   int ub, pages, row, h, cols;
   bool ends;
 };
-__device__ __forceinline__ void axpy(float4& v, float4 x, float f) {
-  v = make_float4(fmaf(x.x, f, v.x), fmaf(x.y, f, v.y), fmaf(x.z, f, v.z), fmaf(x.w, f, v.w));
-}
-
-// A place in the units: page p of tile t of kv head h of session b.
+// A place in the units: page p of kv head h of session b.
 struct Walk {
-  int b, h, t, p, pages;
+  int b, h, p, pages;
   Session s;
   const Session* sess;
-  int B, nkv, rpt;
+  int B, nkv;
   __device__ __forceinline__ void enter(int bb) {  // the first session with work from bb on
     for (b = bb; b < B; ++b) {
       s = sess[b];
       if (s.n) break;
     }
-    h = t = p = 0;
-    pages = b < B ? tile_pages(s.L, s.n, 0, rpt) : 0x7fffffff;
+    h = p = 0;
+    pages = b < B ? tile_pages(s.L, s.n) : 0x7fffffff;
   }
   __device__ __forceinline__ void next_tile() {
     p = 0;
-    if ((t + 1) * rpt < s.n) {
-      ++t;
-    } else {
-      t = 0;
-      if (++h == nkv) {
-        enter(b + 1);
-        return;
-      }
-    }
-    pages = tile_pages(s.L, s.n, t, rpt);
+    if (++h == nkv) enter(b + 1);
   }
   __device__ __forceinline__ void advance(int units) {
     p += units;
@@ -230,9 +190,8 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, ctas_of(NT)) attention_kern
   w.sess = sess;
   w.B = a.q.B;
   w.nkv = a.c.nkv;
-  w.rpt = a.rows_per_tile;
   int u0 = 0, share = 0, units;
-  bool whole = a.one_tile && a.q.bt_stride <= kWholePages;
+  bool whole = a.one_each && a.q.bt_stride <= kWholePages;
   if (!whole) {
     if (warp == 0) {
       int carry = 0, most = 0;
@@ -241,12 +200,11 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, ctas_of(NT)) attention_kern
         if (b0 + lane < a.q.B) {
           const Kv8Session s = kv8_session(a.q, b0 + lane, a.c.max_context, a.c.err);
           sess[b0 + lane] = {s.r0, s.n, s.L};
-          for (int t = 0; t * a.rows_per_tile < s.n; ++t) {
-            const int p = tile_pages(s.L, s.n, t, a.rows_per_tile);
-            x += p;
+          if (s.n) {
+            const int p = tile_pages(s.L, s.n);
             most = max(most, p);
+            x = p * a.c.nkv;
           }
-          x *= a.c.nkv;
         }
         const int own = x;
 #pragma unroll
@@ -265,7 +223,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, ctas_of(NT)) attention_kern
     }
     __syncthreads();
     share = (cum[a.q.B] + gridDim.x - 1) / gridDim.x;
-    whole = a.one_tile && s_most <= max(kWholePages, share + share / 4);
+    whole = a.one_each && s_most <= max(kWholePages, share + share / 4);
   }
   if (whole) {
     share = 0;
@@ -275,8 +233,8 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, ctas_of(NT)) attention_kern
     const Kv8Session s = kv8_session(a.q, w.b, a.c.max_context, a.c.err);
     if (s.n == 0) return;
     w.s = {s.r0, s.n, s.L};
-    w.t = w.p = 0;
-    units = w.pages = tile_pages(s.L, s.n, 0, a.rows_per_tile);
+    w.p = 0;
+    units = w.pages = tile_pages(s.L, s.n);
     w.nkv = w.h + 1;  // nothing follows this tile
     w.B = w.b + 1;
   } else {
@@ -297,10 +255,6 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, ctas_of(NT)) attention_kern
     const int per = (cum[lo + 1] - cum[lo]) / a.c.nkv, rem = u0 - cum[lo];
     w.h = rem / per;
     w.p = rem - w.h * per;
-    while (w.p >= w.pages) {
-      w.p -= w.pages;
-      w.pages = tile_pages(w.s.L, w.s.n, ++w.t, a.rows_per_tile);
-    }
   }
   // this warp's units, as offsets from u0
   const int n0 = (int)((long long)units * warp / W), n1 = (int)((long long)units * (warp + 1) / W);
@@ -333,14 +287,13 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, ctas_of(NT)) attention_kern
   };
   // a column's query and its rotation, as they stand in memory
   auto load_q = [&](RawQuery<KC>& r, int nt) {
-    const int row0 = w.t * a.rows_per_tile, col = nt * 8 + g, qr = col / a.group;
-    const int cols = min(a.rows_per_tile, w.s.n - row0) * a.group;
+    const int col = nt * 8 + g, qr = col / a.group, cols = w.s.n * a.group;
 #pragma unroll
     for (int c = 0; c < KC; ++c)
 #pragma unroll
       for (int e = 0; e < 4; ++e) r.q[c][e] = make_uint2(0u, 0u);
     if (col < cols) {
-      const uint16_t* src = a.qp + (int64_t)(w.s.r0 + row0 + qr) * a.q_stride +
+      const uint16_t* src = a.qp + (int64_t)(w.s.r0 + qr) * a.q_stride +
                             (size_t)(w.h * a.group + col - qr * a.group) * D + 16 * t4;
 #pragma unroll
       for (int c = 0; c < KC; ++c)
@@ -348,7 +301,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, ctas_of(NT)) attention_kern
         for (int e = 0; e < 4; ++e) r.q[c][e] = load8(src + 64 * c + 4 * e);
     }
     if (a.c.rope_cos) {
-      const size_t at = (size_t)(w.s.L + min(row0 + qr, w.s.n - 1)) * (D / 2) + 16 * (D == 128 ? t4 : t4 & 1);
+      const size_t at = (size_t)(w.s.L + min(qr, w.s.n - 1)) * (D / 2) + 16 * (D == 128 ? t4 : t4 & 1);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         r.cs[e] = load16(a.c.rope_cos + at + 4 * e);
@@ -387,9 +340,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, ctas_of(NT)) attention_kern
   while (n < count) {
     const int seg_end = min(count, n + w.pages - w.p);
     const int seg0 = n, p0 = w.p;
-    const int row0 = w.t * a.rows_per_tile;
-    const int rows = min(a.rows_per_tile, w.s.n - row0);
-    const int cols = rows * a.group;
+    const int cols = w.s.n * a.group;
     // queries: rotated, scaled by a power of two per column, as B fragments
     uint32_t qf[NT][KC * 4][2];
     float cf[NT][2];
@@ -450,8 +401,8 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, ctas_of(NT)) attention_kern
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) see[nt][e] = w.s.L + row0 + min((nt * 8 + 2 * t4 + e) / a.group, rows - 1);
-    const int first_masked = (w.s.L + row0 + 1) / kPage;  // pages before this one are seen whole by every row
+      for (int e = 0; e < 2; ++e) see[nt][e] = w.s.L + min((nt * 8 + 2 * t4 + e) / a.group, w.s.n - 1);
+    const int first_masked = (w.s.L + 1) / kPage;  // pages before this one are seen whole by every row
 
     float o[NT][VJ * 2][4], m[NT][2], l[NT][2];
 #pragma unroll
@@ -550,8 +501,15 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, ctas_of(NT)) attention_kern
         for (int e = 0; e < 4; ++e) p[e] = ex2(s[nt][e] - m[nt][e & 1]);
         l[nt][0] += p[0] + p[2];
         l[nt][1] += p[1] + p[3];
-        pf[nt][0] = transpose8(half2_bits(p[0] * sc.y, p[1] * sc.y));
-        pf[nt][1] = transpose8(half2_bits(p[2] * sc.y, p[3] * sc.y));
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = p[e] * sc.y;
+        if (page >= first_masked) {  // what a column does not see gives nothing, whatever its scale
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = p[e] > 0.f || p[e] != p[e] ? v[e] : 0.f;
+        }
+        pf[nt][0] = transpose8(half2_bits(v[0], v[1]));
+        pf[nt][1] = transpose8(half2_bits(v[2], v[3]));
       }
 #pragma unroll
       for (int j = 0; j < VJ; ++j) {
@@ -578,7 +536,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, ctas_of(NT)) attention_kern
     float* dst = piece_col(2 * warp + starts, 0);
     __syncwarp();  // the last copies have been read
     if (!(starts && ends) && lane == 0)
-      s_piece[2 * warp + starts] = {u0 + n0 + seg0 - p0, w.pages, w.s.r0 + row0, w.h, cols, ends};
+      s_piece[2 * warp + starts] = {u0 + n0 + seg0 - p0, w.pages, w.s.r0, w.h, cols, ends};
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -588,7 +546,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, ctas_of(NT)) attention_kern
 #pragma unroll
           for (int j = 0; j < VJ; ++j) {
             const float4 v = make_float4(o[nt][2 * j][e], o[nt][2 * j][e + 2], o[nt][2 * j + 1][e], o[nt][2 * j + 1][e + 2]);
-            if (starts && ends) write(w.s.r0 + row0, w.h, col, 32 * j + 4 * g, v, l[nt][e]);
+            if (starts && ends) write(w.s.r0, w.h, col, 32 * j + 4 * g, v, l[nt][e]);
             else *(float4*)(dst + col * kCol + 32 * j + 4 * g) = v;
           }
           if (!(starts && ends) && g == 0) *(float2*)(dst + col * kCol + D) = make_float2(m[nt][e], l[nt][e]);
@@ -714,7 +672,7 @@ cudaError_t setup_one() {
 template <int D, int NT>
 cudaError_t launch_one(const Args& a, int sms, cudaStream_t s) {
   cudaLaunchConfig_t lc{};
-  lc.gridDim = dim3(a.one_tile && a.q.bt_stride <= kWholePages ? a.q.B * a.c.nkv : sms * ctas_of(NT));
+  lc.gridDim = dim3(a.one_each && a.q.bt_stride <= kWholePages ? a.q.B * a.c.nkv : sms * ctas_of(NT));
   lc.blockDim = dim3(32 * warps_of(NT));
   lc.dynamicSmemBytes = layout(D, NT, a.max_cols, a.q.B).bytes;
   lc.stream = s;
@@ -724,7 +682,8 @@ cudaError_t launch_one(const Args& a, int sms, cudaStream_t s) {
 }  // namespace
 
 cudaError_t kv8_attention_setup(int d) {
-  cudaError_t e;
+  cudaError_t e = kv8_chunk_setup(d);
+  if (e != cudaSuccess) return e;
   if (d == 64) {
     (e = setup_one<64, 1>()) || (e = setup_one<64, 2>()) || (e = setup_one<64, 4>());
   } else {
@@ -736,7 +695,7 @@ cudaError_t kv8_attention_setup(int d) {
 // the arrival counts, then two partial tiles for each CTA of the largest grid
 size_t kv8_attention_workspace(int d, int sms) {
   const size_t ctas = 2 * (size_t)sms;
-  return ctas * sizeof(unsigned) + 2 * ctas * kMaxCols * (d + 4) * sizeof(float);
+  return ctas * sizeof(unsigned) + std::max(2 * ctas * kMaxCols * (d + 4) * sizeof(float), kv8_chunk_workspace(d, sms));
 }
 
 cudaError_t kv8_attention(const Kv8View& v, const Kv8Batch& q, int d, int group, int sms, const uint16_t* qp,
@@ -746,22 +705,23 @@ cudaError_t kv8_attention(const Kv8View& v, const Kv8Batch& q, int d, int group,
   if (q.B * pages * v.nkv >= (1ll << 31) / std::max(tiles, 1ll)) return cudaErrorInvalidValue;
   // the fewest n-tiles that hold every session's columns; more rows go in tiles of 32 columns
   const long long cols = (long long)q.max_new * group;
+  float* part = (float*)((char*)work + 2 * (size_t)sms * sizeof(unsigned));
+  if (cols > kMaxCols)
+    return kv8_chunk(v, q, d, group, sms, qp, q_stride, scale, out, out_stride, (unsigned*)work, part, s);
   const int nt = cols <= 8 ? 1 : cols <= 16 ? 2 : 4;
-  const int rows = 8 * nt / group;
   Args a{};
   a.c = v;
   a.q = q;
   a.group = group;
-  a.rows_per_tile = rows;
-  a.max_cols = (int)std::min(cols, (long long)rows * group);
-  a.one_tile = q.max_new <= rows && (long long)q.B * v.nkv <= sms * ctas_of(nt);
+  a.max_cols = (int)cols;
+  a.one_each = (long long)q.B * v.nkv <= sms * ctas_of(nt);
   a.qp = qp;
   a.q_stride = q_stride;
   a.scale_log2 = scale * kLog2e;
   a.out = out;
   a.out_stride = out_stride;
   a.arrived = (unsigned*)work;
-  a.part = (float*)((char*)work + 2 * (size_t)sms * sizeof(unsigned));
+  a.part = part;
   if (d == 64)
     return nt == 1 ? launch_one<64, 1>(a, sms, s) : nt == 2 ? launch_one<64, 2>(a, sms, s) : launch_one<64, 4>(a, sms, s);
   return nt == 1 ? launch_one<128, 1>(a, sms, s) : nt == 2 ? launch_one<128, 2>(a, sms, s) : launch_one<128, 4>(a, sms, s);
