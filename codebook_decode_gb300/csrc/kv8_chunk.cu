@@ -1,22 +1,21 @@
 // kv8_chunk.cu -- attention of many query rows over the 8-bit paged K/V cache,
 // on the tcgen05 tensor cores (prompts, and batches with prompts among them).
 //
-// A tile is up to 128 rows (query tokens x the q heads of one kv head) of one
-// session. For every 128 keys (8 pages)
+// A tile is up to 128 or 256 rows (query tokens x the q heads of one kv head)
+// of one session. For every 128 keys (8 pages)
 //   S [128 x 128] = Q . K^T,   O [128 x d] += P . V
 // with the accumulators in tensor memory and Q, K, V and P as half in shared
 // memory, in the canonical K-major layout without swizzle. Codes are exact in
 // half; the blocks' scales act outside the products, as in kv8_attention.cu:
 // the K scale on the scores, the V scale on the weights.
 //
-// Warps: two softmax groups of four (a thread per row), which take the key
-// steps in turn, each with its own S, P, O, maximum and sum, so that one
-// group's softmax runs beside the other's products; four warps that widen the
-// codes of the step after into shared memory (once per 128 rows); and one
-// thread that issues the products. The two groups' results are joined at the
-// tile's end. Bound by the softmax and widening instructions next to the
-// products: 128 x 128 scores cost an SM about 1000 cycles of exponentials
-// alone, the two products about 1300.
+// Warps: two softmax groups of four (a thread per row), four warps that widen
+// the codes of the step after into shared memory, and one thread that issues
+// the products. With 256 rows the groups have 128 each and a step's widened
+// codes serve both; with 128 they take the steps in turn, each with its own S,
+// P, O, maximum and sum, which are joined at the tile's end. Either way one
+// group's softmax runs beside the other's products. Bound by the instructions
+// of softmax and widening, which run next to the products.
 //
 // Work is cut into equal shares of key steps, one per CTA; tiles that several
 // CTAs share are joined through the workspace by the last to arrive, in order.
@@ -33,24 +32,30 @@ namespace qtts {
 namespace {
 
 constexpr int kRows = 128, kKeys = 128, kPagesPerStep = kKeys / kPage;
-constexpr int kSoftmaxThreads = 256, kWidenThreads = 128;
-constexpr int kThreadsC = kSoftmaxThreads + kWidenThreads + 32;
+constexpr int kSoftmaxThreads = 256, kWidenThreads = 256;
+constexpr int kThreadsC = kSoftmaxThreads + kWidenThreads + 128;
+// registers of a thread: launched, then of the softmax, widening and issuing groups
+constexpr int kRegsLaunch = 96, kRegsSoftmax = 136, kRegsWiden = 80, kRegsIssue = 48;
+static_assert(kSoftmaxThreads * kRegsSoftmax + kWidenThreads * kRegsWiden + 128 * kRegsIssue <= kThreadsC * kRegsLaunch,
+              "the groups share what the block was launched with");
 constexpr int kChunkTries = 1 << 20;
+constexpr int kJoinSteps = 6;
+constexpr int kIssueWarp = (kSoftmaxThreads + kWidenThreads) / 32;
 
-template <int D>
+template <int D, bool TWO>
 struct ChunkSmem {
-  alignas(1024) uint8_t q[kRows * D * 2];
+  alignas(128) uint8_t q[TWO ? 2 : 1][kRows * D * 2];
   uint8_t p[2][kRows * kKeys * 2];
   uint8_t k[2][kKeys * D * 2];
-  uint8_t v[2][kKeys * D * 2];
-  float2 ml[2][kRows];   // each group's maximum and sum; before the first step the rows' magnitudes
-  float2 sc[4][kPagesPerStep];
-  // kfull, vfull: widened; sdone: the step's scores are there (and its K place is free); pfull: its
-  // weights; pvdone: its second product has run (V and P
-  // places free); qfull: the tile's queries; drained: after a failure, all products issued
-  uint64_t kfull[2], vfull[2], sdone[2], pfull[2], pvdone[2], qfull, drained;
+  uint8_t v[TWO ? 1 : 2][kKeys * D * 2];
+  float2 ml[2][kRows];  // each group's maximum and sum; before the first step the rows' query scales and offsets
+  float4 sc[4][kPagesPerStep];  // a page's K scale, logarithm and reciprocal of its V scale
+  // kfull, vfull: widened; kdone, vdone: read by the products; sdone: a group's
+  // scores are there; pfull: its weights; pvdone: its second product has run;
+  // qfull: the tile's queries; drained: after a failure, all products issued
+  uint64_t kfull[2], vfull[2], kdone[2], vdone[2], sdone[2], pfull[2], pvdone[2], qfull, drained;
   uint32_t tmem;
-  int failed, verdict, flag, share, start_b, start_rem, total;
+  int failed, verdict, flag, share, whole, start_b, start_h, start_t, start_p, total;
 };
 
 struct ChunkArgs {
@@ -62,7 +67,7 @@ struct ChunkArgs {
   float scale_log2, q_sign;  // |softmax scale| log2 e, and its sign
   uint16_t* out;
   int64_t out_stride;
-  float* part;        // [2 CTAs][kRows][D + 4]
+  float* part;        // [2 CTAs][tile rows][D + 4]
   unsigned* arrived;  // [CTAs]
 };
 
@@ -95,14 +100,30 @@ struct Place {
     }
     steps = tile_steps(s.L, s.n, t, a.rows_per_tile);
   }
+  __device__ __forceinline__ void advance(const ChunkArgs& a, int n) {
+    p += n;
+    while (p >= steps) {
+      const int over = p - steps;
+      next_tile(a);
+      p = over;
+    }
+  }
 };
 
-__device__ __forceinline__ int session_steps(const ChunkArgs& a, int b) {
-  if (b >= a.q.B) return 0;
-  const Kv8Session s = kv8_session(a.q, b, a.c.max_context, a.c.err);
-  int w = 0;
-  for (int t = 0; t * a.rows_per_tile < s.n; ++t) w += tile_steps(s.L, s.n, t, a.rows_per_tile);
-  return w * a.c.nkv;
+// A session's tiles, weighed by their key steps (or 1 each: whole), up to the
+// one that brings them past `limit`: returns that tile (or all tiles), `sum` the
+// weight of those before it.
+__device__ __forceinline__ int tiles_until(const Kv8Session& s, int rows_per_tile, bool whole, int limit, int& sum) {
+  const int all = (s.n + rows_per_tile - 1) / rows_per_tile;
+  int t = 0, keys = s.L + rows_per_tile + kKeys - 1;
+  sum = 0;
+#pragma unroll 1
+  for (; t < all; ++t, keys += rows_per_tile) {
+    const int here = whole ? 1 : t + 1 < all ? keys / kKeys : (s.L + s.n + kKeys - 1) / kKeys;
+    if (sum + here > limit) break;
+    sum += here;
+  }
+  return t;
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
@@ -111,6 +132,43 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void softmax_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
+}
+__device__ __forceinline__ void group_sync(int x) {  // one softmax group
+  asm volatile("bar.sync %0, %1;" ::"r"(2 + x), "n"(kSoftmaxThreads / 2) : "memory");
+}
+template <int R>
+__device__ __forceinline__ void set_regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void set_regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// two fp32 at once
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t a) {
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(a));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 constexpr uint32_t idesc_f16(int M, int N) {  // kind::f16: fp32 accumulator, half A and B, both K-major
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
@@ -125,14 +183,18 @@ __device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t at) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(at));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t at) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_ld8(uint32_t (&r)[8], uint32_t at) {
@@ -143,14 +205,19 @@ __device__ __forceinline__ void tmem_ld8(uint32_t (&r)[8], uint32_t at) {
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// codes 0, 1 and 2, 3 of four as 1024 + byte
+__device__ __forceinline__ uint32_t raise_lo(uint32_t c) { return __byte_perm(c, 0x64646464u, 0x4140); }
+__device__ __forceinline__ uint32_t raise_hi(uint32_t c) { return __byte_perm(c, 0x64646464u, 0x4342); }
+
 // The order in which a page's 16 tokens stand along the key axis of both
 // products: that of the V blocks' words. Place n holds token_of(n).
 __host__ __device__ constexpr int token_of(int n) { return 2 * (n >> 2) + (n & 1) + ((n >> 1) & 1) * 8; }
 
-template <int D>
+template <int D, bool TWO>
 __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_constant__ ChunkArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  ChunkSmem<D>& sm = *(ChunkSmem<D>*)smem_raw;
+  using Smem = ChunkSmem<D, TWO>;
+  Smem& sm = *(Smem*)smem_raw;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int kCol = D + 4;
 
@@ -158,7 +225,9 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.kfull[i], kWidenThreads);
       mbar_init(&sm.vfull[i], kWidenThreads);
-      mbar_init(&sm.sdone[i], 1);
+      mbar_init(&sm.kdone[i], 1);
+      mbar_init(&sm.vdone[i], 1);
+      mbar_init(&sm.sdone[i], 2);  // the products, and the issuing thread after it saw the codes' factors
       mbar_init(&sm.pfull[i], kSoftmaxThreads / 2);
       mbar_init(&sm.pvdone[i], 1);
     }
@@ -167,35 +236,64 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
     mbar_init_fence();
     sm.failed = 0;
   }
-  if (warp == 12) {
+  if (warp == kIssueWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sm.tmem)), "n"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  if (warp == 0) {  // shares, and the session in which this CTA's begins
-    int total = 0;
-    for (int b0 = 0; b0 < a.q.B; b0 += 32) total += __reduce_add_sync(0xffffffffu, session_steps(a, b0 + lane));
-    const int share = max((total + (int)gridDim.x - 1) / (int)gridDim.x, 4);
-    const long long u0 = (long long)blockIdx.x * share;
-    int carry = 0;
-    for (int b0 = 0; b0 < a.q.B && u0 < total; b0 += 32) {
-      int x = session_steps(a, b0 + lane);
-      const int own = x;
+  if (warp == 0) {
+    // Shares, and the place where this CTA's begins. Whole tiles where the most
+    // that a CTA gets is not worse than an equal share and the cost of joining
+    // cut tiles (reading queries twice, partials out and in: kJoinSteps).
+    int total = 0, tiles = 0, most = 0, per = 0, own = 0, lo = 0, share = 0;
+    bool whole = false;
+    long long u0 = 0, u1 = 0;
+    Kv8Session ses;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+      int carry = 0;
+#pragma unroll 1
+      for (int b0 = 0; b0 < a.q.B; b0 += 32) {
+        if (!pass || a.q.B > 32) {
+          ses.n = 0;
+          if (b0 + lane < a.q.B) ses = kv8_session(a.q, b0 + lane, a.c.max_context, a.c.err);
+        }
+        const int count = tiles_until(ses, a.rows_per_tile, whole, 0x7fffffff, per);
+        own = per * a.c.nkv;
+        int x = own;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        lo = carry + x - own;
+        carry += __shfl_sync(0xffffffffu, x, 31);
+        if (!pass) {
+          tiles += __reduce_add_sync(0xffffffffu, count * a.c.nkv);
+          most = max(most, __reduce_max_sync(0xffffffffu, ses.n ? (ses.L + ses.n + kKeys - 1) / kKeys : 0));
+        } else if (lo <= u0 && u0 < (long long)lo + own) {
+          const int at = (int)(u0 - lo), h = at / per;
+          int sum;
+          sm.start_b = b0 + lane;
+          sm.start_h = h;
+          sm.start_t = tiles_until(ses, a.rows_per_tile, whole, at - h * per, sum);
+          sm.start_p = at - h * per - sum;
+        }
       }
-      const long long lo = (long long)carry + x - own;
-      if (lo <= u0 && u0 < lo + own) {
-        sm.start_b = b0 + lane;
-        sm.start_rem = (int)(u0 - lo);
+      if (pass == 0) {
+        total = carry;
+        const int G = gridDim.x;
+        share = max((total + G - 1) / G, 4);
+        whole = (long long)((tiles + G - 1) / G) * most <= share + kJoinSteps;
+        u0 = whole ? (long long)tiles * blockIdx.x / G : (long long)blockIdx.x * share;
+        u1 = whole ? (long long)tiles * (blockIdx.x + 1) / G : min(u0 + share, (long long)total);
+        if (u0 >= u1) break;
       }
-      carry += __shfl_sync(0xffffffffu, x, 31);
     }
     if (lane == 0) {
       sm.share = share;
-      sm.total = total;
+      sm.whole = whole;
+      sm.total = (int)max(u1 - u0, 0ll);
     }
   }
   tc_fence_before();
@@ -203,19 +301,24 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
   const int share = sm.share;
-  const long long u0 = (long long)blockIdx.x * share;
-  const int units = u0 < sm.total ? (int)min((long long)share, sm.total - u0) : 0;
+  const long long u0 = (long long)blockIdx.x * share;  // of a cut
+  int units = sm.total;  // key steps of this CTA
   Place w;
   if (units) {
     w.enter(a, sm.start_b);
-    int rem = sm.start_rem, per = session_steps(a, w.b) / a.c.nkv;
-    w.h = rem / per;
-    rem -= w.h * per;
-    while (rem >= w.steps) {
-      rem -= w.steps;
-      w.steps = tile_steps(w.s.L, w.s.n, ++w.t, a.rows_per_tile);
+    w.h = sm.start_h;
+    w.t = sm.start_t;
+    w.p = sm.start_p;
+    w.steps = tile_steps(w.s.L, w.s.n, w.t, a.rows_per_tile);
+    if (sm.whole) {
+      Place x = w;
+      const int tiles = units;
+      units = 0;
+      for (int i = 0; i < tiles; ++i) {
+        units += x.steps;
+        if (i + 1 < tiles) x.next_tile(a);
+      }
     }
-    w.p = rem;
   }
   // bounded; once one wait has run out all others give up too
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -230,168 +333,169 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
   // accumulators: S of group x at 128 x, O at 256 + 128 x
   constexpr uint32_t kSbo = 128, kLboRow = kRows * 16, kLboV = D * 16;
 
-  if (warp >= 8 && warp < 12) {
+  if (warp >= kSoftmaxThreads / 32 && warp < kIssueWarp) {
+    set_regs_down<kRegsWiden>();
     // ---- widen: step j (counted over the CTA) into place j & 1
-    const int t = tid - kSoftmaxThreads;
+    const int wp = warp - kSoftmaxThreads / 32;  // this warp's page of a step
     int j = 0;
     bool ok = true;
-    // K: a warp takes 2 pages of a step, a lane of a load 8 rows x 4 words
-    const int wp = t >> 5;
-    const int r8 = lane & 7, dch = lane >> 3;
-    uint4 kr[D / 16], vr[D / 16];
-    auto blocks = [&](const Place& x, int step, int* out) {  // this warp's pages of the step; -1: beyond the tile
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int pg = step * kPagesPerStep + wp * 2 + i;
-        const int last = (x.s.L + min((x.t + 1) * a.rows_per_tile, x.s.n) - 1) / kPage;
-        out[i] = -1;
-        if (pg <= last) {
+    const int r8 = lane & 7, dch = lane >> 3;  // K: a lane of a load is one of 8 tokens x 4 words
+    constexpr int D4 = D / 4;                  // V: lane x takes the 4 dims 4 x.. (d = 64: of half the words)
+    const int x4 = lane % D4;
+    uint4 kr[D / 32], vr[D / 32];
+    // lane x holds the block of step 32 k + x (-1: beyond the tile); the next 32 steps' are fetched meanwhile
+    Place ahead = w;
+    auto fetch_ids = [&](int k) {
+      int id = -1;
+      if (32 * k + lane < units) {
+        Place x = ahead;
+        x.advance(a, lane);
+        const int pg = x.p * kPagesPerStep + wp;
+        if (pg <= (x.s.L + min((x.t + 1) * a.rows_per_tile, x.s.n) - 1) / kPage) {
           int page = a.q.bt[(size_t)x.b * a.q.bt_stride + pg];
           if (page < 0 || page >= a.c.pool_pages) {
             set_err(a.c.err, QTTS_DEV_BAD_PAGE);
-            page = 0;
+            page = 0;  // inside the pool; the session's result is not used
           }
-          out[i] = page * a.c.nkv + x.h;
+          id = page * a.c.nkv + x.h;
         }
       }
+      if (32 * (k + 1) < units) ahead.advance(a, 32);
+      return id;
     };
     const uint4 none = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);  // codes of 0
-    auto load_k = [&](const int* blk) {
+    auto load_k = [&](int id) {
+      const uint8_t* src = a.c.codes + (size_t)max(id, 0) * (32 * D) + dch * 16;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int n8 = 0; n8 < 2; ++n8)
 #pragma unroll
-        for (int n8 = 0; n8 < 2; ++n8)
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
-            const uint8_t* src = a.c.codes + (size_t)max(blk[i], 0) * (32 * D) + c * 1024 + token_of(n8 * 8 + r8) * 64 + dch * 16;
-            kr[(i * 2 + n8) * (D / 64) + c] = blk[i] >= 0 ? *(const uint4*)src : none;
-          }
+        for (int c = 0; c < D / 64; ++c)
+          kr[n8 * (D / 64) + c] = id >= 0 ? *(const uint4*)(src + c * 1024 + token_of(n8 * 8 + r8) * 64) : none;
     };
-    // V: lane x takes the 4 dims 4x.. (d = 64: half a warp per page) of 8 tokens (two words) at a time
-    constexpr int D4 = D / 4;
-    auto load_v = [&](const int* blk) {
+    auto load_v = [&](int id) {  // d = 128: words t = 0..3; d = 64: t = 2 (lane / 16) + 0, 1
+      const uint8_t* src = a.c.codes + (size_t)max(id, 0) * (32 * D) + 16 * D + x4 * 64 + (D == 128 ? 0 : lane / D4 * 32);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) {  // d = 128: words t = 0..3; d = 64: t = 2 (lane / 16) + 0, 1
-          const int x = lane % D4, tq = D == 128 ? e : 2 * (lane / D4) + e;
-          const uint8_t* src = a.c.codes + (size_t)max(blk[i], 0) * (32 * D) + 16 * D + x * 64 + tq * 16;
-          vr[i * (D / 32) + e] = blk[i] >= 0 ? *(const uint4*)src : none;
-        }
+      for (int e = 0; e < D / 32; ++e) vr[e] = id >= 0 ? *(const uint4*)(src + e * 16) : none;
     };
-    static_assert(2 * 2 * (D / 64) <= D / 16 && 2 * (D / 32) <= D / 16, "registers of a step's words");
-    auto load_scale = [&](const int* b) {
-      float2 v = make_float2(0.f, 0.f);
-      const int mine = lane == 0 ? b[0] : b[1];
-      if (lane < 2 && mine >= 0) v = *(const float2*)(a.c.scales + 2 * (size_t)mine);
-      return v;
+    auto load_scale = [&](int id) {
+      return id >= 0 ? *(const float2*)(a.c.scales + 2 * (size_t)id) : make_float2(0.f, 0.f);
     };
-    Place x = w;  // the step whose block ids were asked for last
-    int left = units, next[2] = {-1, -1};
-    auto advance = [&]() {
-      if (++x.p == x.steps) x.next_tile(a);
-      blocks(x, x.p, next);
-    };
-    float2 sc, sc_next = make_float2(0.f, 0.f);
+    int left = units, ids = -1, ids_next = -1;
+    float2 sc;
     if (left) {
-      blocks(x, x.p, next);
-      sc = load_scale(next);
-      load_k(next);
-      load_v(next);
-      if (left > 1) advance();
+      ids = fetch_ids(0);
+      const int id = __shfl_sync(0xffffffffu, ids, 0);
+      load_k(id);
+      load_v(id);
+      sc = load_scale(id);
     }
     for (; left; ++j, --left) {
-      const int s = j & 1;
-      const uint32_t free_parity = ((j >> 1) - 1) & 1;
-      if (j >= 2) ok = wait(&sm.sdone[s], free_parity);
+      if ((j & 31) == 0) {
+        if (j) ids = ids_next;
+        ids_next = fetch_ids((j >> 5) + 1);
+      }
+      const int id = __shfl_sync(0xffffffffu, (j + 1) & 31 ? ids : ids_next, (j + 1) & 31);  // of the next step
+      const int s = j & 1, vs = TWO ? 0 : s;
+      if (j >= 2) ok = wait(&sm.kdone[s], ((j >> 1) - 1) & 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      if (lane < 2) sm.sc[j & 3][wp * 2 + lane] = sc;
+      if (lane == 0) {
+        const float sv = sc.y != sc.y ? sc.y : fmaxf(sc.y, kKv8MinScale);
+        sm.sc[j & 3][wp] = make_float4(sc.x, lg2(sv), 1.f / sv, 0.f);
+      }
+      uint8_t* kd = sm.k[s] + 2 * dch * kLboRow + wp * 256 + r8 * 16;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int n8 = 0; n8 < 2; ++n8)
 #pragma unroll
-        for (int n8 = 0; n8 < 2; ++n8)
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
-            const uint4 k = kr[(i * 2 + n8) * (D / 64) + c];
-            uint4 lo, hi;  // dims 64 c + 16 dch + 0..7, 8..15
-            widen(k.x, lo.x, lo.y);
-            widen(k.y, lo.z, lo.w);
-            widen(k.z, hi.x, hi.y);
-            widen(k.w, hi.z, hi.w);
-            const int row8 = (wp * 2 + i) * 2 + n8, d8 = 8 * c + 2 * dch;
-            uint8_t* dst = sm.k[s] + (d8 * (kKeys / 8) + row8) * 128 + r8 * 16;
-            *(uint4*)dst = lo;
-            *(uint4*)(dst + kLboRow) = hi;
-          }
+        for (int c = 0; c < D / 64; ++c) {
+          // as 1024 + byte: the score's surplus, 1152 times the query's sum, leaves in the softmax
+          const uint4 k = kr[n8 * (D / 64) + c];
+          uint8_t* dst = kd + 8 * c * kLboRow + n8 * 128;
+          *(uint4*)dst = make_uint4(raise_lo(k.x), raise_hi(k.x), raise_lo(k.y), raise_hi(k.y));
+          *(uint4*)(dst + kLboRow) = make_uint4(raise_lo(k.z), raise_hi(k.z), raise_lo(k.w), raise_hi(k.w));
+        }
       fence_async_shared();
       mbar_arrive(&sm.kfull[s]);
       if (left > 1) {
-        load_k(next);
-        sc_next = load_scale(next);
+        load_k(id);
+        sc = load_scale(id);
       }
-      if (j >= 2) ok = wait(&sm.pvdone[s], free_parity);
+      if (j >= (TWO ? 1 : 2)) ok = wait(&sm.vdone[vs], TWO ? (j - 1) & 1 : ((j >> 1) - 1) & 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       // row r = (D / 4) jd + x4 of the V operand holds dim 4 x4 + jd
+      uint8_t* vd = sm.v[vs] + (wp * 2 + (D == 128 ? 0 : lane / D4)) * (D / 8) * 128 + x4 / 8 * 128 + x4 % 8 * 16;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int h = 0; h < D / 64; ++h) {
+        const uint4 v0 = vr[2 * h], v1 = vr[2 * h + 1];
+        const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
-        for (int h = 0; h < D / 64; ++h) {
-          const int x4 = lane % D4, key8 = (wp * 2 + i) * 2 + (D == 128 ? h : lane / D4);
-          const uint4 v0 = vr[i * (D / 32) + 2 * h], v1 = vr[i * (D / 32) + 2 * h + 1];
-          const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
-#pragma unroll
-          for (int jd = 0; jd < 4; ++jd) {
-            uint4 o;
-            widen(w0[jd], o.x, o.y);
-            widen(w1[jd], o.z, o.w);
-            const int r = jd * D4 + x4;
-            *(uint4*)(sm.v[s] + (key8 * (D / 8) + r / 8) * 128 + r % 8 * 16) = o;
-          }
+        for (int jd = 0; jd < 4; ++jd) {
+          uint4 o;
+          widen(w0[jd], o.x, o.y);
+          widen(w1[jd], o.z, o.w);
+          *(uint4*)(vd + h * (D / 8) * 128 + jd * (D4 / 8) * 128) = o;
         }
+      }
       fence_async_shared();
-      mbar_arrive(&sm.vfull[s]);
-      if (left > 1) load_v(next);
-      if (left > 2) advance();
-      sc = sc_next;
+      mbar_arrive(&sm.vfull[vs]);
+      if (left > 1) load_v(id);
     }
-  } else if (warp == 12) {
+  } else if (warp >= kIssueWarp) {
     // ---- products
-    if (lane == 0) {
+    set_regs_down<kRegsIssue>();
+    if (warp == kIssueWarp && lane == 0) {
       constexpr uint32_t idS = idesc_f16(kRows, kKeys), idO = idesc_f16(kRows, D);
-      const uint32_t qa = smem_addr(sm.q);
-      int j = 0, seg = 0, left = units;
+      int j = 0, seg = 0, left = units, n[2] = {0, 0};  // n: steps of each group
       bool ok = true;
-      auto scores = [&](int jj) {
+      auto scores = [&](int jj, int x, bool last) {  // group x's scores of step jj; last: K's place is free after
         const int s = jj & 1;
         if (!(ok = wait(&sm.kfull[s], (jj >> 1) & 1))) return;
         tc_fence_after();
-        const uint32_t ka = smem_addr(sm.k[s]);
+        const uint32_t qa = smem_addr(sm.q[TWO ? x : 0]), ka = smem_addr(sm.k[s]);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
-          tc_mma(tmem + 128 * s, tc_smem_desc(qa + ks * 2 * kLboRow, kLboRow, kSbo),
+          tc_mma(tmem + 128 * x, tc_smem_desc(qa + ks * 2 * kLboRow, kLboRow, kSbo),
                  tc_smem_desc(ka + ks * 2 * kLboRow, kLboRow, kSbo), idS, ks > 0);
-        tc_commit(&sm.sdone[s]);
+        tc_commit(&sm.sdone[x]);
+        mbar_arrive(&sm.sdone[x]);
+        if (last) tc_commit(&sm.kdone[s]);
+      };
+      auto values = [&](int jj, int x, bool first, bool last) {  // group x's second product of step jj
+        const int vs = TWO ? 0 : jj & 1;
+        ok = wait(&sm.pfull[x], n[x] & 1) && wait(&sm.vfull[vs], TWO ? jj & 1 : (jj >> 1) & 1);
+        if (!ok) return;
+        ++n[x];
+        tc_fence_after();
+        const uint32_t pa = smem_addr(sm.p[x]), va = smem_addr(sm.v[vs]);
+#pragma unroll
+        for (int ks = 0; ks < kKeys / 16; ++ks)
+          tc_mma(tmem + 256 + 128 * x, tc_smem_desc(pa + ks * 2 * kLboRow, kLboRow, kSbo),
+                 tc_smem_desc(va + ks * 2 * kLboV, kLboV, kSbo), idO, !first || ks > 0);
+        tc_commit(&sm.pvdone[x]);
+        if (last) tc_commit(&sm.vdone[vs]);
       };
       while (left && ok) {
-        const int cnt = min(left, w.steps - w.p), j1 = j + cnt, j0 = j;
+        const int cnt = min(left, w.steps - w.p), j0 = j, j1 = j + cnt;
         ok = wait(&sm.qfull, seg & 1);
         tc_fence_after();
-        if (ok) scores(j);
-        if (ok && cnt > 1) scores(j + 1);
-        for (; j < j1 && ok; ++j) {
-          const int s = j & 1;
-          ok = wait(&sm.pfull[s], (j >> 1) & 1) && wait(&sm.vfull[s], (j >> 1) & 1);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t pa = smem_addr(sm.p[s]), va = smem_addr(sm.v[s]);
-#pragma unroll
-          for (int ks = 0; ks < kKeys / 16; ++ks)
-            tc_mma(tmem + 256 + 128 * s, tc_smem_desc(pa + ks * 2 * kLboRow, kLboRow, kSbo),
-                   tc_smem_desc(va + ks * 2 * kLboV, kLboV, kSbo), idO, j - j0 >= 2 || ks > 0);
-          tc_commit(&sm.pvdone[s]);
-          if (j + 2 < j1) scores(j + 2);
+        if constexpr (TWO) {
+          const bool both = min(a.rows_per_tile, w.s.n - w.t * a.rows_per_tile) * a.group > kRows;
+#pragma unroll 1
+          for (int x = 0; x <= both && ok; ++x) scores(j, x, x == both);
+          for (; j < j1 && ok; ++j)
+#pragma unroll 1
+            for (int x = 0; x <= both && ok; ++x) {
+              values(j, x, j == j0, x == both);
+              if (ok && j + 1 < j1) scores(j + 1, x, x == both);
+            }
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < min(cnt, 2) && ok; ++i) scores(j + i, (j + i) & 1, true);
+          for (; j < j1 && ok; ++j) {
+            values(j, j & 1, j - j0 < 2, true);
+            if (ok && j + 2 < j1) scores(j + 2, j & 1, true);
+          }
         }
         left -= cnt;
         ++seg;
@@ -406,74 +510,101 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
     }
     __syncwarp();
   } else {
-    // ---- softmax: thread = row, group x takes the steps of its parity
+    // ---- softmax: thread = row; group x has its own rows, or takes the steps of its parity
+    set_regs_up<kRegsSoftmax>();
     const int x = warp >> 2, row = tid & 127;
     const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + 128 * x + quarter, to = tmem + 256 + quarter;
-    int j = 0, left = units;
+    int j = 0, left = units, n = 0;  // n: steps of this group
     bool ok = true;
     while (left && ok) {
       const int cnt = min(left, w.steps - w.p);
       const int row0 = w.t * a.rows_per_tile, rows = min(a.rows_per_tile, w.s.n - row0), cols = rows * a.group;
-      const int qr = row / a.group;
-      const bool valid = row < cols;
-      const int pos = w.s.L + row0 + min(qr, rows - 1);  // last position that this row sees
-      // this group's half of the row's query: dims D/4 x.. and their partners D/2 further
-      float lo[D / 4], hi[D / 4];
-      {
-        const uint16_t* src = a.qp + (int64_t)(w.s.r0 + row0 + qr) * a.q_stride +
-                              (size_t)(w.h * a.group + row - qr * a.group) * D + x * (D / 4);
+      const int pos = w.s.L + row0 + min((TWO ? tid : row) / a.group, rows - 1);  // last position that this row sees
+      const bool active = !TWO || x == 0 || cols > kRows;
+      // The tile's queries, rotated, into shared memory: a warp takes 8 rows at
+      // a time, lane (r, t) of it 8 dims of row r in every 32, with the partner
+      // dims D/2 further. Scaled by the power of two of the row's largest
+      // magnitude (before the rotation, which can grow it by sqrt 2: half has room).
+      constexpr int kWarpRows = TWO ? 32 : 16;
+      auto load_rows = [&](int r0, uint2 (&raw)[D / 32][2], float4 (&cs)[D / 64][2], float4 (&sn)[D / 64][2]) {
+        const int rr = r0 + (lane & 7), t = lane >> 3, q1 = rr / a.group;
+        const uint16_t* src = a.qp + (int64_t)(w.s.r0 + row0 + q1) * a.q_stride +
+                              (size_t)(w.h * a.group + rr - q1 * a.group) * D + 8 * t;
 #pragma unroll
-        for (int e = 0; e < D / 4; e += 4) {
-          uint2 l2 = make_uint2(0u, 0u), h2 = make_uint2(0u, 0u);
-          if (valid) {
-            l2 = *(const uint2*)(src + e);
-            h2 = *(const uint2*)(src + D / 2 + e);
+        for (int e = 0; e < D / 32; ++e)
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            raw[e][f] = make_uint2(0u, 0u);
+            if (rr < cols) raw[e][f] = *(const uint2*)(src + 32 * e + 4 * f);
           }
-          lo[e] = bf2f(l2.x & 0xffffu);
-          lo[e + 1] = __uint_as_float(l2.x & 0xffff0000u);
-          lo[e + 2] = bf2f(l2.y & 0xffffu);
-          lo[e + 3] = __uint_as_float(l2.y & 0xffff0000u);
-          hi[e] = bf2f(h2.x & 0xffffu);
-          hi[e + 1] = __uint_as_float(h2.x & 0xffff0000u);
-          hi[e + 2] = bf2f(h2.y & 0xffffu);
-          hi[e + 3] = __uint_as_float(h2.y & 0xffff0000u);
-        }
         if (a.c.rope_cos) {
-          const size_t at = (size_t)pos * (D / 2) + x * (D / 4);
+          const size_t at = (size_t)(w.s.L + row0 + min(q1, rows - 1)) * (D / 2) + 8 * t;
 #pragma unroll
-          for (int e = 0; e < D / 4; e += 4) {
-            const float4 c4 = *(const float4*)(a.c.rope_cos + at + e), s4 = *(const float4*)(a.c.rope_sin + at + e);
-            const float cc[4] = {c4.x, c4.y, c4.z, c4.w}, ss[4] = {s4.x, s4.y, s4.z, s4.w};
+          for (int e = 0; e < D / 64; ++e)
 #pragma unroll
-            for (int f = 0; f < 4; ++f) {
-              const float u = lo[e + f], v = hi[e + f];
-              lo[e + f] = u * cc[f] - v * ss[f];
-              hi[e + f] = v * cc[f] + u * ss[f];
+            for (int f = 0; f < 2; ++f) {
+              cs[e][f] = *(const float4*)(a.c.rope_cos + at + 32 * e + 4 * f);
+              sn[e][f] = *(const float4*)(a.c.rope_sin + at + 32 * e + 4 * f);
+            }
+        }
+      };
+      auto put_rows = [&](int r0, uint2 (&raw)[D / 32][2], float4 (&cs)[D / 64][2], float4 (&sn)[D / 64][2]) {
+        const int rr = r0 + (lane & 7), t = lane >> 3;
+        uint32_t mag = 0;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e)
+#pragma unroll
+          for (int f = 0; f < 2; ++f) mag = __vmaxu2(mag, __vmaxu2(raw[e][f].x & 0x7fff7fffu, raw[e][f].y & 0x7fff7fffu));
+        mag = max(mag & 0xffffu, mag >> 16);
+        mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 8));
+        mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 16));
+        const uint32_t ex = min(max(mag << 16 & 0x7f800000u, 1u << 23), 253u << 23);
+        const float inv = __uint_as_float((254u << 23) - ex) * a.q_sign;
+        float sum = 0.f;  // of the row's halves
+        uint8_t* base = sm.q[TWO ? rr >> 7 : 0] + (rr & 127) / 8 * 128 + rr % 8 * 16;
+#pragma unroll
+        for (int e = 0; e < D / 64; ++e) {
+          const uint2 l0 = raw[e][0], l1 = raw[e][1], h0 = raw[e + D / 64][0], h1 = raw[e + D / 64][1];
+          const uint32_t wl[4] = {l0.x, l0.y, l1.x, l1.y}, wh[4] = {h0.x, h0.y, h1.x, h1.y};
+          const float cv[8] = {cs[e][0].x, cs[e][0].y, cs[e][0].z, cs[e][0].w, cs[e][1].x, cs[e][1].y, cs[e][1].z, cs[e][1].w};
+          const float sv[8] = {sn[e][0].x, sn[e][0].y, sn[e][0].z, sn[e][0].w, sn[e][1].x, sn[e][1].y, sn[e][1].z, sn[e][1].w};
+          float u[8], v[8];
+#pragma unroll
+          for (int f = 0; f < 8; ++f) {
+            const float p = (f & 1 ? __uint_as_float(wl[f / 2] & 0xffff0000u) : bf2f(wl[f / 2] & 0xffffu)) * inv;
+            const float q = (f & 1 ? __uint_as_float(wh[f / 2] & 0xffff0000u) : bf2f(wh[f / 2] & 0xffffu)) * inv;
+            u[f] = p;
+            v[f] = q;
+            if (a.c.rope_cos) {
+              u[f] = p * cv[f] - q * sv[f];
+              v[f] = q * cv[f] + p * sv[f];
             }
           }
+          uint8_t* dst = base + (4 * e + t) * kLboRow;
+          const uint32_t hu[8] = {half2_bits(u[0], u[1]), half2_bits(u[2], u[3]), half2_bits(u[4], u[5]), half2_bits(u[6], u[7]),
+                                  half2_bits(v[0], v[1]), half2_bits(v[2], v[3]), half2_bits(v[4], v[5]), half2_bits(v[6], v[7])};
+#pragma unroll
+          for (int f = 0; f < 8; ++f) {
+            const float2 y = __half22float2(*(const __half2*)&hu[f]);
+            sum += y.x + y.y;
+          }
+          *(uint4*)dst = make_uint4(hu[0], hu[1], hu[2], hu[3]);
+          *(uint4*)(dst + D / 16 * kLboRow) = make_uint4(hu[4], hu[5], hu[6], hu[7]);
         }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        if (t == 0) sm.ml[TWO ? rr >> 7 : 1][rr & 127] = make_float2(__uint_as_float(ex) * a.scale_log2, 1152.f * sum);
+      };
+#pragma unroll 1
+      for (int r0 = kWarpRows * warp; r0 < min(kWarpRows * (warp + 1), cols); r0 += 8) {
+        uint2 raw[D / 32][2];
+        float4 c[D / 64][2], s[D / 64][2];
+        load_rows(r0, raw, c, s);
+        put_rows(r0, raw, c, s);
       }
-      uint32_t mxe = 0;
-#pragma unroll
-      for (int e = 0; e < D / 4; ++e)
-        mxe = max(mxe, max(__float_as_uint(lo[e]) & 0x7f800000u, __float_as_uint(hi[e]) & 0x7f800000u));
-      sm.ml[x][row].x = __uint_as_float(mxe);
       softmax_sync();
-      mxe = max(mxe, __float_as_uint(sm.ml[x ^ 1][row].x));
-      const uint32_t ex = min(max(mxe, 1u << 23), 253u << 23);
-      const float inv = __uint_as_float((254u << 23) - ex) * a.q_sign;
-      const float cf = __uint_as_float(ex) * a.scale_log2;
-#pragma unroll
-      for (int e = 0; e < D / 4; e += 8) {
-        const int d8 = (x * (D / 4) + e) / 8;
-        uint8_t* dst = sm.q + (d8 * (kRows / 8) + row / 8) * 128 + row % 8 * 16;
-        *(uint4*)dst = make_uint4(half2_bits(lo[e] * inv, lo[e + 1] * inv), half2_bits(lo[e + 2] * inv, lo[e + 3] * inv),
-                                  half2_bits(lo[e + 4] * inv, lo[e + 5] * inv), half2_bits(lo[e + 6] * inv, lo[e + 7] * inv));
-        *(uint4*)(dst + D / 16 * kLboRow) =
-            make_uint4(half2_bits(hi[e] * inv, hi[e + 1] * inv), half2_bits(hi[e + 2] * inv, hi[e + 3] * inv),
-                       half2_bits(hi[e + 4] * inv, hi[e + 5] * inv), half2_bits(hi[e + 6] * inv, hi[e + 7] * inv));
-      }
+      const float cf = sm.ml[TWO ? x : 1][row].x, surplus = sm.ml[TWO ? x : 1][row].y;
       fence_async_shared();
       tc_fence_before();  // the last tile's accumulators have been read
       mbar_arrive(&sm.qfull);
@@ -482,42 +613,51 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
       int mine = 0;  // steps of this group in this tile
       const int first_masked = (w.s.L + row0 + 1) / kKeys;
       for (int i = 0; i < cnt && ok; ++i, ++j) {
-        if ((j & 1) != x) continue;
-        const uint32_t parity = (j >> 1) & 1;
-        ok = wait(&sm.kfull[x], parity) && wait(&sm.sdone[x], parity);
+        if (TWO ? !active : (j & 1) != x) continue;
+        ok = wait(&sm.sdone[x], n & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
         const int step = w.p + i;
-        const bool masked = step >= first_masked;
-        const int lim = pos - step * kKeys;  // keys of the step that the row sees: places <= lim
-        const float2* sc = sm.sc[j & 3];
-        // largest score (with the V scale's logarithm, see kv8_attention.cu)
-        float mx = kNone;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t r[32];
-          tmem_ld32(r, ts + 32 * c);
+        const int lim = pos - step * kKeys;  // keys of the step that the row sees: those at <= lim
+        const float4* sc = sm.sc[j & 3];
+        uint32_t r[2][32];  // half of the row's scores at a time
+        auto load_scores = [&](int half) {
+          tmem_ld32(r[0], ts + 64 * half);
+          tmem_ld32(r[1], ts + 64 * half + 32);
           tmem_wait_ld();
+          if (step >= first_masked) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float g = -INFINITY;
-            if (masked) {
+            for (int n = 0; n < 64; ++n)
+              if (64 * half + n / kPage * kPage + token_of(n % kPage) > lim) r[n / 32][n % 32] = 0xff800000u;  // -inf
+          }
+        };
+        // a page's factors: of one that the row does not see at all they are
+        // harmless ones, whatever its scales
+        auto factors = [&](int page) {
+          float4 f = sc[page];
+          if (page * kPage > lim) f = make_float4(1.f, 0.f, 1.f, 0.f);
+          f.x = fmaxf(f.x * cf, kKv8MinScale) + (f.x != f.x ? f.x : 0.f);  // positive: -inf stays -inf
+          f.y = fmaf(-surplus, f.x, f.y);
+          return f;
+        };
+        float mx = kNone;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          load_scores(half);
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (32 * c + 16 * h + token_of(e) <= lim) g = fmaxf(g, __uint_as_float(r[16 * h + e]));
-            } else {
+          for (int page = 0; page < kPagesPerStep / 2; ++page) {
+            auto at = [&](int e) { return __uint_as_float(r[page / 2][page % 2 * 16 + e]); };
+            float g = max3(at(0), at(1), at(2));
 #pragma unroll
-              for (int e = 0; e < 16; ++e) g = fmaxf(g, __uint_as_float(r[16 * h + e]));
-            }
-            const float2 s2 = sc[2 * c + h];
-            const float lv = lg2(fmaxf(s2.y, kKv8MinScale));
-            const float v = fmaf(g, s2.x * cf, lv);
-            mx = fmaxf(mx, g > -INFINITY ? v : kNone);
+            for (int e = 3; e < 15; e += 2) g = max3(g, at(e), at(e + 1));
+            g = fmaxf(g, at(15));
+            const float4 f = factors(half * (kPagesPerStep / 2) + page);
+            mx = fmaxf(mx, fmaf(g, f.x, f.y));
           }
         }
         // the product before last of this group frees its weights' place and its O
-        if (j >= 2) ok = wait(&sm.pvdone[x], ((j >> 1) - 1) & 1);
+        if (n) ok = wait(&sm.pvdone[x], (n - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const bool grow = mx > m + kSlack;
@@ -528,55 +668,48 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
           if (mine) {
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t r[32];
-              tmem_ld32(r, to + 128 * x + 32 * c);
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld16(o, to + 128 * x + 16 * c);
               tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
-              tmem_st32(to + 128 * x + 32 * c, r);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st16(to + 128 * x + 16 * c, o);
             }
             tmem_wait_st();
           }
         }
         uint8_t* dst = sm.p[x] + row / 8 * 128 + row % 8 * 16;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half, dst += 8 * kLboRow) {
+          load_scores(half);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t r[32];
-          tmem_ld32(r, ts + 32 * c);
-          tmem_wait_ld();
+          for (int page = 0; page < kPagesPerStep / 2; ++page) {
+            const float4 f = factors(half * (kPagesPerStep / 2) + page);
+            const uint64_t mul = pack2(f.x, f.x), off = pack2(f.y - m, f.y - m);
+            uint64_t sum = 0;
+            uint32_t h[8];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float2 s2 = sc[2 * c + h];
-            const float f = s2.x * cf;
-            float p[16], sum = 0.f;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              p[e] = ex2(fmaf(__uint_as_float(r[16 * h + e]), f, -m));
-              if (masked && 32 * c + 16 * h + token_of(e) > lim) p[e] = 0.f;
+            for (int e = 0; e < 8; ++e) {
+              const uint32_t* s2 = &r[page / 2][page % 2 * 16 + 2 * e];
+              const float2 y = unpack2(fma2(pack2(__uint_as_float(s2[0]), __uint_as_float(s2[1])), mul, off));
+              const float p0 = ex2(y.x), p1 = ex2(y.y);  // weight times V scale
+              sum = add2(sum, pack2(p0, p1));
+              h[e] = half2_bits(p0, p1);
             }
-#pragma unroll
-            for (int e = 0; e < 16; ++e) sum += p[e];
-            l += sum;
-            // a page that the row does not see gives nothing, whatever its scale
-            const float sv = masked && 32 * c + 16 * h > lim ? 0.f : s2.y;
-#pragma unroll
-            for (int q8 = 0; q8 < 2; ++q8)
-              *(uint4*)(dst + (4 * c + 2 * h + q8) * kLboRow) =
-                  make_uint4(half2_bits(p[8 * q8] * sv, p[8 * q8 + 1] * sv), half2_bits(p[8 * q8 + 2] * sv, p[8 * q8 + 3] * sv),
-                             half2_bits(p[8 * q8 + 4] * sv, p[8 * q8 + 5] * sv), half2_bits(p[8 * q8 + 6] * sv, p[8 * q8 + 7] * sv));
+            const float2 t = unpack2(sum);
+            l = fmaf(t.x + t.y, f.z, l);
+            *(uint4*)(dst + 2 * page * kLboRow) = make_uint4(h[0], h[1], h[2], h[3]);
+            *(uint4*)(dst + (2 * page + 1) * kLboRow) = make_uint4(h[4], h[5], h[6], h[7]);
           }
         }
         fence_async_shared();
         tc_fence_before();
         mbar_arrive(&sm.pfull[x]);
         ++mine;
+        ++n;
       }
-      // the group's last product
-      if (ok && mine) {
-        const int last = (j - 1 - (((j - 1) & 1) != x)) >> 1;
-        ok = wait(&sm.pvdone[x], last & 1);
-      }
+      if (ok && mine) ok = wait(&sm.pvdone[x], (n - 1) & 1);  // the group's last product
       ok = __all_sync(0xffffffffu, ok);
       sm.ml[x][row] = make_float2(m, l);
       softmax_sync();
@@ -584,46 +717,74 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
       softmax_sync();
       if (sm.verdict) break;
       tc_fence_after();
-      const float2 mlA = sm.ml[0][row], mlB = sm.ml[1][row];
-      const float mj = fmaxf(mlA.x, mlB.x), fA = ex2(mlA.x - mj), fB = ex2(mlB.x - mj);
-      const float sum = mlA.y * fA + mlB.y * fB;
-      const bool hasA = cnt > 1 || ((j - 1) & 1) == 0, hasB = cnt > 1 || ((j - 1) & 1) == 1;
+      // maximum and sum of row r; with the groups on the same rows also their factors
+      auto joined = [&](int r, float& fA, float& fB) {
+        if (TWO) return sm.ml[x][r & 127];
+        const float2 mlA = sm.ml[0][r], mlB = sm.ml[1][r];
+        const float mj = fmaxf(mlA.x, mlB.x);
+        fA = ex2(mlA.x - mj);
+        fB = ex2(mlB.x - mj);
+        return make_float2(mj, mlA.y * fA + mlB.y * fB);
+      };
+      float fA = 1.f, fB = 1.f;
+      joined(row, fA, fB);
+      const bool hasA = TWO ? x == 0 : cnt > 1 || ((j - 1) & 1) == 0, hasB = TWO ? x == 1 : cnt > 1 || ((j - 1) & 1) == 1;
       const bool starts = w.p == 0, ends = w.p + cnt == w.steps;
       const long long ub = u0 + (units - left) - w.p;
       const int c0 = (int)(ub / share), pieces = (int)((ub + w.steps - 1) / share) - c0 + 1;
-      float* part = a.part + ((size_t)(2 * blockIdx.x + starts) * kRows + row) * kCol;
-      uint16_t* out = a.out + (int64_t)(w.s.r0 + row0 + qr) * a.out_stride + (size_t)(w.h * a.group + row - qr * a.group) * D;
-      // this group writes half of the dims: columns jd D/4 + y of O hold dim 4 y + jd
+      constexpr int kTile = TWO ? 2 * kRows : kRows;
+      auto write = [&](int r, int y, float4 v, float inv_sum) {
+        const int rq = r / a.group;
+        uint16_t* o = a.out + (int64_t)(w.s.r0 + row0 + rq) * a.out_stride + (size_t)(w.h * a.group + r - rq * a.group) * D + 4 * y;
+        *(uint2*)o = make_uint2(f2bf(v.x * inv_sum) | (uint32_t)f2bf(v.y * inv_sum) << 16,
+                                f2bf(v.z * inv_sum) | (uint32_t)f2bf(v.w * inv_sum) << 16);
+      };
+      // Half of the dims at a time through shared memory (the group's weights'
+      // place), so that a row is written by neighbouring lanes: row r's 16-byte
+      // word y stands at y ^ (r mod D / 8). Columns jd D/4 + y of O hold dim 4 y + jd.
+      constexpr int kHalf = D / 8;
+      float4* tile = (float4*)sm.p[x];
 #pragma unroll 1
-      for (int y0 = x * (D / 8); y0 < (x + 1) * (D / 8); y0 += 8) {
-        float o[4][8];
+      for (int half = TWO ? 0 : x; half <= (TWO ? 1 : x) && active; ++half) {
+#pragma unroll 1
+        for (int y0 = 0; y0 < kHalf; y0 += 8) {
+          float o[4][8];
 #pragma unroll
-        for (int jd = 0; jd < 4; ++jd) {
-          uint32_t rA[8], rB[8];
-          if (hasA) tmem_ld8(rA, to + jd * (D / 4) + y0);
-          if (hasB) tmem_ld8(rB, to + 128 + jd * (D / 4) + y0);
-          tmem_wait_ld();
+          for (int jd = 0; jd < 4; ++jd) {
+            uint32_t rA[8], rB[8];
+            if (hasA) tmem_ld8(rA, to + jd * (D / 4) + half * kHalf + y0);
+            if (hasB) tmem_ld8(rB, to + 128 + jd * (D / 4) + half * kHalf + y0);
+            tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            o[jd][e] = 0.f;
-            if (hasA) o[jd][e] = __uint_as_float(rA[e]) * fA;
-            if (hasB) o[jd][e] = fmaf(__uint_as_float(rB[e]), fB, o[jd][e]);
+            for (int e = 0; e < 8; ++e) {
+              o[jd][e] = 0.f;
+              if (hasA) o[jd][e] = __uint_as_float(rA[e]) * fA;
+              if (hasB) o[jd][e] = fmaf(__uint_as_float(rB[e]), fB, o[jd][e]);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            tile[row * kHalf + ((y0 + e) ^ (row & (kHalf - 1)))] = make_float4(o[0][e], o[1][e], o[2][e], o[3][e]);
+        }
+        group_sync(x);
+        for (int r1 = (warp & 3) * (32 / kHalf); r1 < kRows; r1 += 4 * (32 / kHalf)) {
+          const int rl = r1 + lane / kHalf, y = lane % kHalf, r = TWO ? 128 * x + rl : rl;
+          if (r < cols) {
+            const float4 v = tile[rl * kHalf + (y ^ (rl & (kHalf - 1)))];
+            float f0, f1;
+            const float2 ml = joined(r, f0, f1);
+            if (starts && ends) {
+              write(r, half * kHalf + y, v, 1.f / ml.y);
+            } else {
+              float* part = a.part + ((size_t)(2 * blockIdx.x + starts) * kTile + r) * kCol;
+              *(float4*)(part + 4 * (half * kHalf + y)) = v;
+              if (y == 0) *(float2*)(part + D) = ml;
+            }
           }
         }
-        if (valid && starts && ends) {
-          const float r = 1.f / sum;
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            *(uint2*)(out + 4 * (y0 + e)) = make_uint2(f2bf(o[0][e] * r) | (uint32_t)f2bf(o[1][e] * r) << 16,
-                                                       f2bf(o[2][e] * r) | (uint32_t)f2bf(o[3][e] * r) << 16);
-        } else if (valid) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            *(float4*)(part + 4 * (y0 + e)) = make_float4(o[0][e], o[1][e], o[2][e], o[3][e]);
-        }
+        group_sync(x);
       }
       if (!(starts && ends)) {
-        if (valid && x == 0) *(float2*)(part + D) = make_float2(mj, sum);
         __threadfence();
         softmax_sync();
         if (tid == 0) {
@@ -634,7 +795,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
         if (sm.flag) {
           __threadfence();
           for (int r = warp; r < cols; r += kSoftmaxThreads / 32) {
-            auto partial = [&](int i) { return a.part + ((size_t)(2 * (c0 + i) + (i == 0)) * kRows + r) * kCol; };
+            auto partial = [&](int i) { return a.part + ((size_t)(2 * (c0 + i) + (i == 0)) * kTile + r) * kCol; };
             float mm = kNone, ss = 0.f;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int i0 = 0; i0 < pieces; i0 += 32) {
@@ -655,16 +816,11 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
                 for (int e = 0; e < 4; ++e) axpy(v, y[e], __shfl_sync(0xffffffffu, f1, k + e));
               }
             }
-            if (lane < D / 4) {
-              const int rq = r / a.group;
-              const float inv_sum = 1.f / ss;
-              uint16_t* o = a.out + (int64_t)(w.s.r0 + row0 + rq) * a.out_stride + (size_t)(w.h * a.group + r - rq * a.group) * D + 4 * lane;
-              *(uint2*)o = make_uint2(f2bf(v.x * inv_sum) | (uint32_t)f2bf(v.y * inv_sum) << 16,
-                                      f2bf(v.z * inv_sum) | (uint32_t)f2bf(v.w * inv_sum) << 16);
-            }
+            if (lane < D / 4) write(r, lane, v, 1.f / ss);
           }
         }
       }
+      softmax_sync();  // this tile's maxima and sums have been read
       left -= cnt;
       w.p += cnt;
       if (w.p == w.steps) w.next_tile(a);
@@ -673,37 +829,45 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12)
+  if (warp == kIssueWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512) : "memory");
 }
 
-static_assert(sizeof(ChunkSmem<128>) <= 227 * 1024, "shared memory of a CTA");
+static_assert(sizeof(ChunkSmem<128, true>) <= 227 * 1024 && sizeof(ChunkSmem<128, false>) <= 227 * 1024,
+              "shared memory of a CTA");
 
-template <int D>
+template <int D, bool TWO>
 cudaError_t launch_chunk(const ChunkArgs& a, int sms, cudaStream_t s) {
   cudaLaunchConfig_t lc{};
   lc.gridDim = dim3(sms);
   lc.blockDim = dim3(kThreadsC);
-  lc.dynamicSmemBytes = sizeof(ChunkSmem<D>);
+  lc.dynamicSmemBytes = sizeof(ChunkSmem<D, TWO>);
   lc.stream = s;
-  return cudaLaunchKernelEx(&lc, chunk_kernel<D>, a);
+  return cudaLaunchKernelEx(&lc, chunk_kernel<D, TWO>, a);
+}
+template <int D, bool TWO>
+cudaError_t setup_chunk() {
+  return cudaFuncSetAttribute(chunk_kernel<D, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(ChunkSmem<D, TWO>));
 }
 
 }  // namespace
 
 cudaError_t kv8_chunk_setup(int d) {
-  return d == 64 ? cudaFuncSetAttribute(chunk_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(ChunkSmem<64>))
-                 : cudaFuncSetAttribute(chunk_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(ChunkSmem<128>));
+  cudaError_t e = d == 64 ? setup_chunk<64, false>() : setup_chunk<128, false>();
+  if (e == cudaSuccess) e = d == 64 ? setup_chunk<64, true>() : setup_chunk<128, true>();
+  return e;
 }
 
-size_t kv8_chunk_workspace(int d, int sms) { return 2 * (size_t)sms * kRows * (d + 4) * sizeof(float); }
+size_t kv8_chunk_workspace(int d, int sms) { return 2 * (size_t)sms * 2 * kRows * (d + 4) * sizeof(float); }
 
 cudaError_t kv8_chunk(const Kv8View& v, const Kv8Batch& q, int d, int group, int sms, const uint16_t* qp,
                       int64_t q_stride, float scale, uint16_t* out, int64_t out_stride, unsigned* arrived, float* part,
                       cudaStream_t s) {
-  ChunkArgs a{v, q, group, kRows / group, qp, q_stride, std::fabs(scale) * kLog2e, scale < 0.f ? -1.f : 1.f, out,
-              out_stride, part, arrived};
-  return d == 64 ? launch_chunk<64>(a, sms, s) : launch_chunk<128>(a, sms, s);
+  const bool two = (long long)q.n_rows * group * v.nkv >= 2ll * sms * 2 * kRows;
+  ChunkArgs a{v, q, group, (two ? 2 : 1) * kRows / group, qp, q_stride, std::fabs(scale) * kLog2e,
+              scale < 0.f ? -1.f : 1.f, out, out_stride, part, arrived};
+  if (d == 64) return two ? launch_chunk<64, true>(a, sms, s) : launch_chunk<64, false>(a, sms, s);
+  return two ? launch_chunk<128, true>(a, sms, s) : launch_chunk<128, false>(a, sms, s);
 }
 
 }  // namespace qtts
