@@ -61,7 +61,7 @@ struct ChunkSmem {
 struct ChunkArgs {
   Kv8View c;
   Kv8Batch q;
-  int group, rows_per_tile;
+  int group, rows_per_tile, group_mul;  // r / group = r * group_mul >> 16 for r < 256
   const uint16_t* qp;
   int64_t q_stride;
   float scale_log2, q_sign;  // |softmax scale| log2 e, and its sign
@@ -223,8 +223,8 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.kfull[i], kWidenThreads);
-      mbar_init(&sm.vfull[i], kWidenThreads);
+      mbar_init(&sm.kfull[i], kWidenThreads / 2);
+      mbar_init(&sm.vfull[i], kWidenThreads / 2);
       mbar_init(&sm.kdone[i], 1);
       mbar_init(&sm.vdone[i], 1);
       mbar_init(&sm.sdone[i], 2);  // the products, and the issuing thread after it saw the codes' factors
@@ -330,27 +330,28 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
     set_err(a.c.err, QTTS_DEV_TIMEOUT);
     return false;
   };
+  auto row_of = [&](int r) { return r * a.group_mul >> 16; };  // a tile row's query row
   // accumulators: S of group x at 128 x, O at 256 + 128 x
   constexpr uint32_t kSbo = 128, kLboRow = kRows * 16, kLboV = D * 16;
 
   if (warp >= kSoftmaxThreads / 32 && warp < kIssueWarp) {
     set_regs_down<kRegsWiden>();
     // ---- widen: step j (counted over the CTA) into place j & 1
-    const int wp = warp - kSoftmaxThreads / 32;  // this warp's page of a step
+    // four warps for K, four for V, so that neither waits for the other's place;
+    // a warp takes 2 of a step's pages
+    const bool is_v = warp >= kSoftmaxThreads / 32 + 4;
+    const int wp = (warp & 3) * 2;
     int j = 0;
     bool ok = true;
-    const int r8 = lane & 7, dch = lane >> 3;  // K: a lane of a load is one of 8 tokens x 4 words
-    constexpr int D4 = D / 4;                  // V: lane x takes the 4 dims 4 x.. (d = 64: of half the words)
-    const int x4 = lane % D4;
-    uint4 kr[D / 32], vr[D / 32];
-    // lane x holds the block of step 32 k + x (-1: beyond the tile); the next 32 steps' are fetched meanwhile
+    // lane x holds the block of page x & 1 of this warp's two, of step 16 k + x / 2
+    // (-1: beyond the tile); the next 16 steps' are fetched meanwhile
     Place ahead = w;
     auto fetch_ids = [&](int k) {
       int id = -1;
-      if (32 * k + lane < units) {
+      if (16 * k + (lane >> 1) < units) {
         Place x = ahead;
-        x.advance(a, lane);
-        const int pg = x.p * kPagesPerStep + wp;
+        x.advance(a, lane >> 1);
+        const int pg = x.p * kPagesPerStep + wp + (lane & 1);
         if (pg <= (x.s.L + min((x.t + 1) * a.rows_per_tile, x.s.n) - 1) / kPage) {
           int page = a.q.bt[(size_t)x.b * a.q.bt_stride + pg];
           if (page < 0 || page >= a.c.pool_pages) {
@@ -360,86 +361,87 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
           id = page * a.c.nkv + x.h;
         }
       }
-      if (32 * (k + 1) < units) ahead.advance(a, 32);
+      if (16 * (k + 1) < units) ahead.advance(a, 16);
       return id;
     };
-    const uint4 none = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);  // codes of 0
-    auto load_k = [&](int id) {
-      const uint8_t* src = a.c.codes + (size_t)max(id, 0) * (32 * D) + dch * 16;
-#pragma unroll
-      for (int n8 = 0; n8 < 2; ++n8)
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c)
-          kr[n8 * (D / 64) + c] = id >= 0 ? *(const uint4*)(src + c * 1024 + token_of(n8 * 8 + r8) * 64) : none;
-    };
-    auto load_v = [&](int id) {  // d = 128: words t = 0..3; d = 64: t = 2 (lane / 16) + 0, 1
-      const uint8_t* src = a.c.codes + (size_t)max(id, 0) * (32 * D) + 16 * D + x4 * 64 + (D == 128 ? 0 : lane / D4 * 32);
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) vr[e] = id >= 0 ? *(const uint4*)(src + e * 16) : none;
-    };
-    auto load_scale = [&](int id) {
-      return id >= 0 ? *(const float2*)(a.c.scales + 2 * (size_t)id) : make_float2(0.f, 0.f);
-    };
     int left = units, ids = -1, ids_next = -1;
-    float2 sc;
+    // K: a lane of a load is one of 8 tokens x 4 words. V: lane x takes the 4 dims
+    // 4x.. (d = 64: of half the words)
+    constexpr int D4 = D / 4, kWords = D / 32;  // 16-byte words of a lane and page
+    const int r8 = lane & 7, dch = lane >> 3, x4 = lane % D4;
+    const size_t lane_at = is_v ? 16 * D + x4 * 64 + (D == 128 ? 0 : lane / D4 * 32) : dch * 16;
+    uint4 wd[2][kWords];
+    float2 sc[2];
+    auto load = [&](int step) {
+      const int from = (step ^ j) & 16 ? ids_next : ids;
+      const uint4 none = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);  // codes of 0
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int id = __shfl_sync(0xffffffffu, from, 2 * (step & 15) + i);
+        const uint8_t* src = a.c.codes + (size_t)max(id, 0) * (32 * D) + lane_at;
+#pragma unroll
+        for (int e = 0; e < kWords; ++e) {
+          const int at = is_v ? e * 16 : e % (D / 64) * 1024 + token_of(e / (D / 64) * 8 + r8) * 64;
+          wd[i][e] = id >= 0 ? *(const uint4*)(src + at) : none;
+        }
+        sc[i] = !is_v && id >= 0 ? *(const float2*)(a.c.scales + 2 * (size_t)id) : make_float2(0.f, 0.f);
+      }
+    };
     if (left) {
       ids = fetch_ids(0);
-      const int id = __shfl_sync(0xffffffffu, ids, 0);
-      load_k(id);
-      load_v(id);
-      sc = load_scale(id);
+      load(0);
     }
     for (; left; ++j, --left) {
-      if ((j & 31) == 0) {
+      if ((j & 15) == 0) {
         if (j) ids = ids_next;
-        ids_next = fetch_ids((j >> 5) + 1);
+        ids_next = fetch_ids((j >> 4) + 1);
       }
-      const int id = __shfl_sync(0xffffffffu, (j + 1) & 31 ? ids : ids_next, (j + 1) & 31);  // of the next step
-      const int s = j & 1, vs = TWO ? 0 : s;
-      if (j >= 2) ok = wait(&sm.kdone[s], ((j >> 1) - 1) & 1);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      if (lane == 0) {
-        const float sv = sc.y != sc.y ? sc.y : fmaxf(sc.y, kKv8MinScale);
-        sm.sc[j & 3][wp] = make_float4(sc.x, lg2(sv), 1.f / sv, 0.f);
-      }
-      uint8_t* kd = sm.k[s] + 2 * dch * kLboRow + wp * 256 + r8 * 16;
-#pragma unroll
-      for (int n8 = 0; n8 < 2; ++n8)
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          // as 1024 + byte: the score's surplus, 1152 times the query's sum, leaves in the softmax
-          const uint4 k = kr[n8 * (D / 64) + c];
-          uint8_t* dst = kd + 8 * c * kLboRow + n8 * 128;
-          *(uint4*)dst = make_uint4(raise_lo(k.x), raise_hi(k.x), raise_lo(k.y), raise_hi(k.y));
-          *(uint4*)(dst + kLboRow) = make_uint4(raise_lo(k.z), raise_hi(k.z), raise_lo(k.w), raise_hi(k.w));
+      const int s = j & 1;
+      if (!is_v) {
+        if (j >= 2) ok = wait(&sm.kdone[s], ((j >> 1) - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane < 2) {
+          const float2 v = lane ? sc[1] : sc[0];
+          const float sv = v.y != v.y ? v.y : fmaxf(v.y, kKv8MinScale);
+          sm.sc[j & 3][wp + lane] = make_float4(v.x, lg2(sv), 1.f / sv, 0.f);
         }
-      fence_async_shared();
-      mbar_arrive(&sm.kfull[s]);
-      if (left > 1) {
-        load_k(id);
-        sc = load_scale(id);
-      }
-      if (j >= (TWO ? 1 : 2)) ok = wait(&sm.vdone[vs], TWO ? (j - 1) & 1 : ((j >> 1) - 1) & 1);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      // row r = (D / 4) jd + x4 of the V operand holds dim 4 x4 + jd
-      uint8_t* vd = sm.v[vs] + (wp * 2 + (D == 128 ? 0 : lane / D4)) * (D / 8) * 128 + x4 / 8 * 128 + x4 % 8 * 16;
+        uint8_t* kd = sm.k[s] + 2 * dch * kLboRow + wp * 256 + r8 * 16;
 #pragma unroll
-      for (int h = 0; h < D / 64; ++h) {
-        const uint4 v0 = vr[2 * h], v1 = vr[2 * h + 1];
-        const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int jd = 0; jd < 4; ++jd) {
-          uint4 o;
-          widen(w0[jd], o.x, o.y);
-          widen(w1[jd], o.z, o.w);
-          *(uint4*)(vd + h * (D / 8) * 128 + jd * (D4 / 8) * 128) = o;
-        }
+          for (int e = 0; e < kWords; ++e) {
+            // as 1024 + byte: the score's surplus, 1152 times the query's sum, leaves in the softmax
+            const uint4 k = wd[i][e];
+            uint8_t* dst = kd + i * 256 + 8 * (e % (D / 64)) * kLboRow + e / (D / 64) * 128;
+            *(uint4*)dst = make_uint4(raise_lo(k.x), raise_hi(k.x), raise_lo(k.y), raise_hi(k.y));
+            *(uint4*)(dst + kLboRow) = make_uint4(raise_lo(k.z), raise_hi(k.z), raise_lo(k.w), raise_hi(k.w));
+          }
+      } else {
+        const int vs = TWO ? 0 : s;
+        if (j >= (TWO ? 1 : 2)) ok = wait(&sm.vdone[vs], TWO ? (j - 1) & 1 : ((j >> 1) - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        // row r = (D / 4) jd + x4 of the V operand holds dim 4 x4 + jd
+        uint8_t* vd = sm.v[vs] + (wp * 2 + (D == 128 ? 0 : lane / D4)) * (D / 8) * 128 + x4 / 8 * 128 + x4 % 8 * 16;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int h = 0; h < kWords / 2; ++h) {
+            const uint4 v0 = wd[i][2 * h], v1 = wd[i][2 * h + 1];
+            const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+            for (int jd = 0; jd < 4; ++jd) {
+              uint4 o;
+              widen(w0[jd], o.x, o.y);
+              widen(w1[jd], o.z, o.w);
+              *(uint4*)(vd + (2 * i + h) * (D / 8) * 128 + jd * (D4 / 8) * 128) = o;
+            }
+          }
       }
       fence_async_shared();
-      mbar_arrive(&sm.vfull[vs]);
-      if (left > 1) load_v(id);
+      mbar_arrive(is_v ? &sm.vfull[TWO ? 0 : s] : &sm.kfull[s]);
+      if (left > 1) load(j + 1);
     }
   } else if (warp >= kIssueWarp) {
     // ---- products
@@ -520,7 +522,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
     while (left && ok) {
       const int cnt = min(left, w.steps - w.p);
       const int row0 = w.t * a.rows_per_tile, rows = min(a.rows_per_tile, w.s.n - row0), cols = rows * a.group;
-      const int pos = w.s.L + row0 + min((TWO ? tid : row) / a.group, rows - 1);  // last position that this row sees
+      const int pos = w.s.L + row0 + min(row_of(TWO ? tid : row), rows - 1);  // last position that this row sees
       const bool active = !TWO || x == 0 || cols > kRows;
       // The tile's queries, rotated, into shared memory: a warp takes 8 rows at
       // a time, lane (r, t) of it 8 dims of row r in every 32, with the partner
@@ -528,7 +530,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
       // magnitude (before the rotation, which can grow it by sqrt 2: half has room).
       constexpr int kWarpRows = TWO ? 32 : 16;
       auto load_rows = [&](int r0, uint2 (&raw)[D / 32][2], float4 (&cs)[D / 64][2], float4 (&sn)[D / 64][2]) {
-        const int rr = r0 + (lane & 7), t = lane >> 3, q1 = rr / a.group;
+        const int rr = r0 + (lane & 7), t = lane >> 3, q1 = row_of(rr);
         const uint16_t* src = a.qp + (int64_t)(w.s.r0 + row0 + q1) * a.q_stride +
                               (size_t)(w.h * a.group + rr - q1 * a.group) * D + 8 * t;
 #pragma unroll
@@ -597,11 +599,13 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
         if (t == 0) sm.ml[TWO ? rr >> 7 : 1][rr & 127] = make_float2(__uint_as_float(ex) * a.scale_log2, 1152.f * sum);
       };
 #pragma unroll 1
-      for (int r0 = kWarpRows * warp; r0 < min(kWarpRows * (warp + 1), cols); r0 += 8) {
-        uint2 raw[D / 32][2];
-        float4 c[D / 64][2], s[D / 64][2];
-        load_rows(r0, raw, c, s);
-        put_rows(r0, raw, c, s);
+      for (int r0 = kWarpRows * warp; r0 < min(kWarpRows * (warp + 1), cols); r0 += 16) {
+        uint2 raw[2][D / 32][2];
+        float4 c[2][D / 64][2], s[2][D / 64][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) load_rows(r0 + 8 * i, raw[i], c[i], s[i]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) put_rows(r0 + 8 * i, raw[i], c[i], s[i]);
       }
       softmax_sync();
       const float cf = sm.ml[TWO ? x : 1][row].x, surplus = sm.ml[TWO ? x : 1][row].y;
@@ -717,24 +721,26 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
       softmax_sync();
       if (sm.verdict) break;
       tc_fence_after();
-      // maximum and sum of row r; with the groups on the same rows also their factors
-      auto joined = [&](int r, float& fA, float& fB) {
-        if (TWO) return sm.ml[x][r & 127];
-        const float2 mlA = sm.ml[0][r], mlB = sm.ml[1][r];
+      // the row's maximum and sum; with both groups on the same rows their factors, and the joined ones
+      float fA = 1.f, fB = 1.f;
+      float2 ml = sm.ml[x][row];
+      if (!TWO) {
+        const float2 mlA = sm.ml[0][row], mlB = sm.ml[1][row];
         const float mj = fmaxf(mlA.x, mlB.x);
         fA = ex2(mlA.x - mj);
         fB = ex2(mlB.x - mj);
-        return make_float2(mj, mlA.y * fA + mlB.y * fB);
-      };
-      float fA = 1.f, fB = 1.f;
-      joined(row, fA, fB);
+        ml = make_float2(mj, mlA.y * fA + mlB.y * fB);
+      }
+      softmax_sync();
       const bool hasA = TWO ? x == 0 : cnt > 1 || ((j - 1) & 1) == 0, hasB = TWO ? x == 1 : cnt > 1 || ((j - 1) & 1) == 1;
       const bool starts = w.p == 0, ends = w.p + cnt == w.steps;
       const long long ub = u0 + (units - left) - w.p;
       const int c0 = (int)(ub / share), pieces = (int)((ub + w.steps - 1) / share) - c0 + 1;
+      if (starts && ends) ml.y = 1.f / ml.y;
+      sm.ml[x][row] = ml;
       constexpr int kTile = TWO ? 2 * kRows : kRows;
       auto write = [&](int r, int y, float4 v, float inv_sum) {
-        const int rq = r / a.group;
+        const int rq = row_of(r);
         uint16_t* o = a.out + (int64_t)(w.s.r0 + row0 + rq) * a.out_stride + (size_t)(w.h * a.group + r - rq * a.group) * D + 4 * y;
         *(uint2*)o = make_uint2(f2bf(v.x * inv_sum) | (uint32_t)f2bf(v.y * inv_sum) << 16,
                                 f2bf(v.z * inv_sum) | (uint32_t)f2bf(v.w * inv_sum) << 16);
@@ -767,14 +773,14 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
             tile[row * kHalf + ((y0 + e) ^ (row & (kHalf - 1)))] = make_float4(o[0][e], o[1][e], o[2][e], o[3][e]);
         }
         group_sync(x);
-        for (int r1 = (warp & 3) * (32 / kHalf); r1 < kRows; r1 += 4 * (32 / kHalf)) {
+#pragma unroll 2
+        for (int r1 = (warp & 3) * (32 / kHalf); r1 < min(kRows, cols - (TWO ? 128 * x : 0)); r1 += 4 * (32 / kHalf)) {
           const int rl = r1 + lane / kHalf, y = lane % kHalf, r = TWO ? 128 * x + rl : rl;
           if (r < cols) {
             const float4 v = tile[rl * kHalf + (y ^ (rl & (kHalf - 1)))];
-            float f0, f1;
-            const float2 ml = joined(r, f0, f1);
+            const float2 ml = sm.ml[x][rl];
             if (starts && ends) {
-              write(r, half * kHalf + y, v, 1.f / ml.y);
+              write(r, half * kHalf + y, v, ml.y);
             } else {
               float* part = a.part + ((size_t)(2 * blockIdx.x + starts) * kTile + r) * kCol;
               *(float4*)(part + 4 * (half * kHalf + y)) = v;
@@ -864,7 +870,7 @@ cudaError_t kv8_chunk(const Kv8View& v, const Kv8Batch& q, int d, int group, int
                       int64_t q_stride, float scale, uint16_t* out, int64_t out_stride, unsigned* arrived, float* part,
                       cudaStream_t s) {
   const bool two = (long long)q.n_rows * group * v.nkv >= 2ll * sms * 2 * kRows;
-  ChunkArgs a{v, q, group, (two ? 2 : 1) * kRows / group, qp, q_stride, std::fabs(scale) * kLog2e,
+  ChunkArgs a{v, q, group, (two ? 2 : 1) * kRows / group, (65536 + group - 1) / group, qp, q_stride, std::fabs(scale) * kLog2e,
               scale < 0.f ? -1.f : 1.f, out, out_stride, part, arrived};
   if (d == 64) return two ? launch_chunk<64, true>(a, sms, s) : launch_chunk<64, false>(a, sms, s);
   return two ? launch_chunk<128, true>(a, sms, s) : launch_chunk<128, false>(a, sms, s);
