@@ -44,6 +44,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kW4Rows = 16, kW4K = 64, kW4MaxM = 64;
 constexpr int kW4Warps = 8, kW4Threads = 32 * kW4Warps;
+constexpr int kW4MaxSplit = 4;  // CTAs of a cluster; clusters of 8 left SMs of a GPC unused and ran in two waves
 
 // scales of one row block and k tile of 64 (groups of 32), or of one group
 __host__ __device__ __forceinline__ int scale_units(int KT, int K, int group) { return group == 32 ? KT : K / group; }
@@ -140,13 +141,19 @@ struct W4Args {
   void* y;
   int64_t y_stride;
   int y_f32;
-  int rw;  // warps along the row blocks; kW4Warps / rw along k
+  int rw_log, s_log;  // 2^rw_log warps along the row blocks, the others along k; clusters of 2^s_log CTAs
+  int chunk;  // k tiles of activations in shared memory at a time
 };
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 // Two codes to a bf16 pair: 4 bits under the exponent of 2^7 are 128 + code +
 // 8, minus 136 the code itself, exactly.
@@ -164,22 +171,32 @@ __device__ __forceinline__ uint4 load_stream(const uint4* p) {
   return v;
 }
 
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+
 // A CTA's warps stand rw along the row blocks (R blocks each) and 8 / rw along
 // k, and the CTAs of a cluster split k further; partial sums meet in shared
-// memory, across the cluster through distributed shared memory.
+// memory, across the cluster through distributed shared memory. The CTA's
+// range of the activations is copied to shared memory (all rows, `chunk` k
+// tiles at a time) while the first weights are on their way; without it every
+// k tile waited for its activations.
 template <int NT, int R>
-__global__ void __launch_bounds__(kW4Threads) w4_kernel(const __grid_constant__ W4Args a) {
-  extern __shared__ float part[];  // [k warps][8 NT][rows + 4]
+__global__ void __launch_bounds__(kW4Threads, NT <= 4 ? 2 : 1) w4_kernel(const __grid_constant__ W4Args a) {
+  extern __shared__ __align__(16) uint8_t w4_smem[];  // activations, then the sums [k warps][8 NT][rows + 4]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   cg::cluster_group cluster = cg::this_cluster();
-  const int S = cluster.num_blocks(), rank = cluster.block_rank();
-  const int kw = kW4Warps / a.rw, wr = warp % a.rw, wk = warp / a.rw;
-  const int cta_rows = 16 * R * a.rw, stride = cta_rows + 4;
-  const int rb0 = ((blockIdx.x / S) * a.rw + wr) * R;
-  const int p = rank * kw + wk, parts = S * kw;
-  const int k0 = (int)((long long)a.KT * p / parts), k1 = (int)((long long)a.KT * (p + 1) / parts);
+  const int S = 1 << a.s_log, rank = blockIdx.x & (S - 1), cta = blockIdx.x >> a.s_log;
+  const int rw = 1 << a.rw_log, kw_log = 3 - a.rw_log, kw = 1 << kw_log, wr = warp & (rw - 1), wk = warp >> a.rw_log;
+  const int cta_rows = 16 * R << a.rw_log, stride = cta_rows + 4;
+  const int rb0 = ((cta << a.rw_log) + wr) * R;
+  const int t0 = a.KT * rank >> a.s_log, t1 = a.KT * (rank + 1) >> a.s_log;
   const bool fine = a.group == 32;
-  const int tiles_per_group = a.group == 128 ? 2 : 1;
+  const int unit_log = a.group == 128 ? 1 : 0;  // k tiles of a unit of scales
+  const uint4* codes = a.codes + (size_t)rb0 * a.KT * 32 + lane;
+  const uint16_t* scales = a.scales + (fine ? (size_t)rb0 * a.sunits * 32 + 4 * g : (size_t)rb0 * a.sunits * 16 + 2 * g);
+  const size_t codes_step = (size_t)a.KT * 32, scales_step = (size_t)a.sunits * (fine ? 32 : 16);  // to the next row block
+  const int pitch = a.chunk * kW4K * 2 + 64;  // bytes of a row: rows 2i and 2i + 1 on different banks
 
   float acc[R][NT][4];
 #pragma unroll
@@ -189,76 +206,98 @@ __global__ void __launch_bounds__(kW4Threads) w4_kernel(const __grid_constant__ 
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[r][nt][e] = 0.f;
 
-  constexpr int P = NT == 1 ? 4 : 2;  // tiles in flight
+  constexpr int P = R == 1 ? 6 : 4;  // tiles in flight
   uint4 w[P][R];
   uint2 sc[P][R];
-  auto fetch = [&](int i, int kt) {
+  for (int c0 = t0; c0 < t1; c0 += a.chunk) {
+    const int c1 = min(c0 + a.chunk, t1), n = c1 - c0;
+    const int k0 = c0 + (n * wk >> kw_log), k1 = c0 + (n * (wk + 1) >> kw_log);
+    auto fetch = [&](int i, int kt) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      w[i][r] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
-      sc[i][r] = make_uint2(0u, 0u);
-      if (kt < k1 && rb0 + r < a.RB) {
-        w[i][r] = load_stream(a.codes + ((size_t)(rb0 + r) * a.KT + kt) * 32 + lane);
-        if (fine)
-          sc[i][r] = *(const uint2*)(a.scales + ((size_t)(rb0 + r) * a.sunits + kt) * 32 + 4 * g);
-        else
-          sc[i][r].x = *(const uint32_t*)(a.scales + ((size_t)(rb0 + r) * a.sunits + kt / tiles_per_group) * 16 + 2 * g);
+      for (int r = 0; r < R; ++r) {
+        w[i][r] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+        sc[i][r] = make_uint2(0u, 0u);
+        if (kt < k1 && rb0 + r < a.RB) {
+          w[i][r] = load_stream(codes + r * codes_step + kt * 32);
+          if (fine) sc[i][r] = *(const uint2*)(scales + r * scales_step + kt * 32);
+          else sc[i][r].x = *(const uint32_t*)(scales + r * scales_step + (kt >> unit_log) * 16);
+        }
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < P; ++i) fetch(i, k0 + i);
+    // activations: 16 bytes are 8 k; beyond K zeros (the codes there are 0)
+    const int per_row = n * (kW4K / 8), have = min(per_row, a.K / 8 - c0 * (kW4K / 8));
+    if (c0 > t0) __syncthreads();  // the last chunk has been read
+    for (int m = warp; m < a.M; m += kW4Warps) {
+      uint8_t* dst = w4_smem + (size_t)m * pitch;
+      const uint16_t* src = a.x + (int64_t)m * a.x_stride + c0 * kW4K;
+#pragma unroll 4
+      for (int c = lane; c < per_row; c += 32) {
+        if (c < have) copy16(dst + c * 16, src + c * 8);
+        else *(uint4*)(dst + c * 16) = make_uint4(0u, 0u, 0u, 0u);
       }
     }
-  };
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    for (int kt = k0; kt < k1; kt += P) {
 #pragma unroll
-  for (int i = 0; i < P; ++i) fetch(i, k0 + i);
-  const uint16_t* xr = a.x + (int64_t)g * a.x_stride + 8 * t;
-  for (int kt = k0; kt < k1; kt += P) {
+      for (int i = 0; i < P; ++i) {
+        if (kt + i < k1) {
+          uint4 b[NT][2];
+          const uint8_t* xs = w4_smem + (size_t)g * pitch + (kt + i - c0) * (kW4K * 2) + 16 * t;
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      if (kt + i < k1) {
-        uint4 b[NT][2];
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            b[nt][h] = make_uint4(0u, 0u, 0u, 0u);
-            const int k = (kt + i) * kW4K + 32 * h;
-            if (nt * 8 + g < a.M && k < a.K) b[nt][h] = *(const uint4*)(xr + (int64_t)nt * 8 * a.x_stride + k);
-          }
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const uint32_t words[4] = {w[i][r].x, w[i][r].y, w[i][r].z, w[i][r].w};
-          float s[2][2];  // [row half][32-k half]
-          if (fine) {
-            s[0][0] = bf2f(sc[i][r].x & 0xffffu);
-            s[0][1] = __uint_as_float(sc[i][r].x & 0xffff0000u);
-            s[1][0] = bf2f(sc[i][r].y & 0xffffu);
-            s[1][1] = __uint_as_float(sc[i][r].y & 0xffff0000u);
-          } else {
-            s[0][0] = s[0][1] = bf2f(sc[i][r].x & 0xffffu);
-            s[1][0] = s[1][1] = __uint_as_float(sc[i][r].x & 0xffff0000u);
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t av[2][4];
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) av[e][j] = widen4(words[2 * h + e] >> (4 * j));
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              float c[4] = {0.f, 0.f, 0.f, 0.f};
-              mma_bf16(c, av[0], b[nt][h].x, b[nt][h].y);
-              mma_bf16(c, av[1], b[nt][h].z, b[nt][h].w);
-              acc[r][nt][0] = fmaf(c[0], s[0][h], acc[r][nt][0]);
-              acc[r][nt][1] = fmaf(c[1], s[0][h], acc[r][nt][1]);
-              acc[r][nt][2] = fmaf(c[2], s[1][h], acc[r][nt][2]);
-              acc[r][nt][3] = fmaf(c[3], s[1][h], acc[r][nt][3]);
+            for (int h = 0; h < 2; ++h) {
+              b[nt][h] = make_uint4(0u, 0u, 0u, 0u);
+              if (nt * 8 + g < a.M) b[nt][h] = *(const uint4*)(xs + (size_t)nt * 8 * pitch + 64 * h);
             }
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const uint32_t words[4] = {w[i][r].x, w[i][r].y, w[i][r].z, w[i][r].w};
+            float s[2][2];  // [row half][32-k half]
+            if (fine) {
+              s[0][0] = bf2f(sc[i][r].x & 0xffffu);
+              s[0][1] = __uint_as_float(sc[i][r].x & 0xffff0000u);
+              s[1][0] = bf2f(sc[i][r].y & 0xffffu);
+              s[1][1] = __uint_as_float(sc[i][r].y & 0xffff0000u);
+            } else {
+              s[0][0] = s[0][1] = bf2f(sc[i][r].x & 0xffffu);
+              s[1][0] = s[1][1] = __uint_as_float(sc[i][r].x & 0xffff0000u);
+            }
+            float c[NT][4];
+            auto flush = [&](int h) {
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[r][nt][e] = fmaf(c[nt][e], s[e >> 1][h], acc[r][nt][e]);
+            };
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t av[2][4];
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) av[e][j] = widen4(words[2 * h + e] >> (4 * j));
+              if (h == 1 && fine) flush(0);  // groups of 32 end inside the tile
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                if (h == 0 || fine) mma_bf16_first(c[nt], av[0], b[nt][h].x, b[nt][h].y);
+                else mma_bf16(c[nt], av[0], b[nt][h].x, b[nt][h].y);
+                mma_bf16(c[nt], av[1], b[nt][h].z, b[nt][h].w);
+              }
+            }
+            flush(1);
           }
+          fetch(i, kt + i + P);
         }
-        fetch(i, kt + i + P);
       }
     }
   }
 
+  float* part = (float*)w4_smem;
+  __syncthreads();  // the activations have been read
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -266,36 +305,58 @@ __global__ void __launch_bounds__(kW4Threads) w4_kernel(const __grid_constant__ 
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         part[(wk * 8 * NT + nt * 8 + 2 * t + (e & 1)) * stride + (wr * R + r) * 16 + g + 8 * (e >> 1)] = acc[r][nt][e];
-  if (S > 1) cluster.sync();
-  else __syncthreads();
-  const int n0 = (blockIdx.x / S) * cta_rows;
-  for (int idx = rank * kW4Threads + threadIdx.x; idx < cta_rows * a.M; idx += S * kW4Threads) {
-    const int m = idx / cta_rows, n = idx % cta_rows;
-    float v = 0.f;
-    for (int c = 0; c < S; ++c) {
-      const float* src = S > 1 ? cluster.map_shared_rank(part, c) : part;
-      for (int k = 0; k < kw; ++k) v += src[(k * 8 * NT + m) * stride + n];
-    }
+  __syncthreads();
+  const int n0 = cta * cta_rows, shift = 31 - __clz(cta_rows);  // cta_rows is a power of two
+  auto put = [&](int m, int n, float v) {
     if (n0 + n < a.N) {
       if (a.y_f32) ((float*)a.y)[(int64_t)m * a.y_stride + n0 + n] = v;
       else ((uint16_t*)a.y)[(int64_t)m * a.y_stride + n0 + n] = f2bf(v);
     }
+  };
+  // over the k warps, then (all loads at once: each crosses the SMs) over the cluster
+  for (int idx = threadIdx.x; idx < cta_rows * a.M; idx += kW4Threads) {
+    const int m = idx >> shift, n = idx & (cta_rows - 1);
+    float v = 0.f;
+#pragma unroll
+    for (int k = 0; k < kW4Warps; ++k)
+      if (k < kw) v += part[(k * 8 * NT + m) * stride + n];
+    if (S == 1) put(m, n, v);
+    else part[m * stride + n] = v;
   }
-  if (S > 1) cluster.sync();  // no CTA leaves while another reads its sums
+  if (S == 1) return;
+  cluster.sync();
+  for (int idx = rank * kW4Threads + threadIdx.x; idx < cta_rows * a.M; idx += S * kW4Threads) {
+    const int m = idx >> shift, n = idx & (cta_rows - 1);
+    float v[kW4MaxSplit];
+#pragma unroll
+    for (int c = 0; c < kW4MaxSplit; ++c) v[c] = c < S ? cluster.map_shared_rank(part, c)[m * stride + n] : 0.f;
+#pragma unroll
+    for (int c = 1; c < kW4MaxSplit; ++c) v[0] += v[c];
+    put(m, n, v[0]);
+  }
+  cluster.sync();  // no CTA leaves while another reads its sums
 }
 
-// partial sums of the widest form: rw = 4, 2 k warps
+constexpr int kW4Smem = 200 * 1024;  // at most
+
+template <int NT, int R>
+cudaError_t w4_setup_one() {
+  return cudaFuncSetAttribute(w4_kernel<NT, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, kW4Smem);
+}
 cudaError_t w4_setup() {
-  return cudaFuncSetAttribute(w4_kernel<8, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * 64 * (128 + 4) * 4);
+  cudaError_t e;
+  (e = w4_setup_one<1, 1>()) || (e = w4_setup_one<2, 2>()) || (e = w4_setup_one<4, 2>()) || (e = w4_setup_one<8, 2>());
+  return e;
 }
 
 template <int NT, int R>
-cudaError_t w4_launch(const W4Args& a, int S, cudaStream_t s) {
-  const int kw = kW4Warps / a.rw, cta_rows = 16 * R * a.rw;
+cudaError_t w4_launch(W4Args a, cudaStream_t s) {
+  const int S = 1 << a.s_log, kw = kW4Warps >> a.rw_log, cta_rows = 16 * R << a.rw_log;
+  a.chunk = std::min((a.KT + S - 1) / S, (kW4Smem / a.M - 64) / (kW4K * 2));
   cudaLaunchConfig_t lc{};
   lc.gridDim = dim3((a.N + cta_rows - 1) / cta_rows * S);
   lc.blockDim = dim3(kW4Threads);
-  lc.dynamicSmemBytes = (size_t)kw * 8 * NT * (cta_rows + 4) * sizeof(float);
+  lc.dynamicSmemBytes = std::max((size_t)a.M * (a.chunk * kW4K * 2 + 64), (size_t)kw * 8 * NT * (cta_rows + 4) * sizeof(float));
   lc.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -480,19 +541,18 @@ int qtts_w4_linear(qtts_w4* w, int M, const uint16_t* x, int64_t x_stride, void*
   DeviceGuard g(w->device);
   if (!g.ok) return fail(w, QTTS_E_CUDA, "cudaSetDevice failed");
   W4Args a{w->codes, w->scales, w->N, w->K, w->RB, w->KT, w->group, scale_units(w->KT, w->K, w->group),
-           M, x, x_stride, y, y_stride, y_dtype == QTTS_DTYPE_F32, 1};
+           M, x, x_stride, y, y_stride, y_dtype == QTTS_DTYPE_F32, 0, 0, 0};
   cudaError_t e;
   const cudaStream_t s = (cudaStream_t)stream;
-  int S = 1;
-  if (M <= 8) {
-    while (S < 8 && w->RB * S < w->G && w->KT >= 2 * S * 2 * kW4Warps) S *= 2;
-    e = w4_launch<1, 1>(a, S, s);
-  } else {
-    a.rw = 4;
-    const int ctas = (w->RB + 7) / 8;
-    while (S < 8 && ctas * S < w->G && w->KT >= 2 * S * 2 * 2) S *= 2;
-    e = M <= 16 ? w4_launch<2, 2>(a, S, s) : M <= 32 ? w4_launch<4, 2>(a, S, s) : w4_launch<8, 2>(a, S, s);
-  }
+  // Up to 8 rows: 16 weight rows a CTA, its warps along k (activations are few,
+  // weights spread over all SMs). More rows: 64 weight rows a CTA, so that fewer
+  // CTAs copy the activations. Clusters along k until the SMs have a CTA each and
+  // while every warp keeps two k tiles.
+  a.rw_log = M <= 8 ? 0 : 1;
+  const int ctas = M <= 8 ? w->RB : (w->RB + 3) / 4, kw = kW4Warps >> a.rw_log;
+  while ((1 << a.s_log) < kW4MaxSplit && ctas << a.s_log < w->G && w->KT >= (4 * kw) << a.s_log) ++a.s_log;
+  if (M <= 8) e = w4_launch<1, 1>(a, s);
+  else e = M <= 16 ? w4_launch<2, 2>(a, s) : M <= 32 ? w4_launch<4, 2>(a, s) : w4_launch<8, 2>(a, s);
   if (e != cudaSuccess) return fail(w, QTTS_E_CUDA, "qtts_w4_linear: %s", cudaGetErrorString(e));
   return QTTS_OK;
 }
