@@ -171,6 +171,17 @@ __device__ __forceinline__ uint4 load_stream(const uint4* p) {
   return v;
 }
 
+// Loads that stay where they are written, ahead of their use.
+__device__ __forceinline__ uint2 load_early8(const void* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t load_early4(const void* p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
 __device__ __forceinline__ void copy16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
 }
@@ -182,7 +193,7 @@ __device__ __forceinline__ void copy16(void* dst, const void* src) {
 // tiles at a time) while the first weights are on their way; without it every
 // k tile waited for its activations.
 template <int NT, int R>
-__global__ void __launch_bounds__(kW4Threads, NT <= 4 ? 2 : 1) w4_kernel(const __grid_constant__ W4Args a) {
+__global__ void __launch_bounds__(kW4Threads, NT <= 2 ? 2 : 1) w4_kernel(const __grid_constant__ W4Args a) {
   extern __shared__ __align__(16) uint8_t w4_smem[];  // activations, then the sums [k warps][8 NT][rows + 4]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   cg::cluster_group cluster = cg::this_cluster();
@@ -206,7 +217,10 @@ __global__ void __launch_bounds__(kW4Threads, NT <= 4 ? 2 : 1) w4_kernel(const _
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[r][nt][e] = 0.f;
 
-  constexpr int P = R == 1 ? 6 : 4;  // tiles in flight
+  int row_at[NT];  // a column's activation row (beyond M any: it is not written)
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) row_at[nt] = min(nt * 8 + g, a.M - 1) * pitch;
+  constexpr int P = R == 1 ? 6 : NT == 4 ? 6 : 4;  // tiles in flight
   uint4 w[P][R];
   uint2 sc[P][R];
   for (int c0 = t0; c0 < t1; c0 += a.chunk) {
@@ -215,12 +229,10 @@ __global__ void __launch_bounds__(kW4Threads, NT <= 4 ? 2 : 1) w4_kernel(const _
     auto fetch = [&](int i, int kt) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        w[i][r] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
-        sc[i][r] = make_uint2(0u, 0u);
-        if (kt < k1 && rb0 + r < a.RB) {
+        if (kt < k1 && rb0 + r < a.RB) {  // else nothing that is read, or rows that are not written
           w[i][r] = load_stream(codes + r * codes_step + kt * 32);
-          if (fine) sc[i][r] = *(const uint2*)(scales + r * scales_step + kt * 32);
-          else sc[i][r].x = *(const uint32_t*)(scales + r * scales_step + (kt >> unit_log) * 16);
+          if (fine) sc[i][r] = load_early8(scales + r * scales_step + kt * 32);
+          else sc[i][r].x = load_early4(scales + r * scales_step + (kt >> unit_log) * 16);
         }
       }
     };
@@ -245,13 +257,12 @@ __global__ void __launch_bounds__(kW4Threads, NT <= 4 ? 2 : 1) w4_kernel(const _
       for (int i = 0; i < P; ++i) {
         if (kt + i < k1) {
           uint4 b[NT][2];
-          const uint8_t* xs = w4_smem + (size_t)g * pitch + (kt + i - c0) * (kW4K * 2) + 16 * t;
+          const uint8_t* xs = w4_smem + (kt + i - c0) * (kW4K * 2) + 16 * t;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              b[nt][h] = make_uint4(0u, 0u, 0u, 0u);
-              if (nt * 8 + g < a.M) b[nt][h] = *(const uint4*)(xs + (size_t)nt * 8 * pitch + 64 * h);
+              b[nt][h] = *(const uint4*)(xs + row_at[nt] + 64 * h);
             }
 #pragma unroll
           for (int r = 0; r < R; ++r) {
