@@ -5,6 +5,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_runtime.h>
 #include <stdint.h>
 
 namespace qtts {
@@ -82,5 +83,20 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
 }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+
+// Programmatic dependent launch: a kernel launched so may start while the one
+// before it on the stream still runs, and waits here, before it reads or writes
+// anything that others touch, until that one has completed. Its own followers
+// may come as soon as all of its blocks are here.
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+inline void early_launch(cudaLaunchConfig_t& lc, cudaLaunchAttribute* at) {
+  at[lc.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[lc.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = at;
+  ++lc.numAttrs;
+}
 
 }  // namespace qtts

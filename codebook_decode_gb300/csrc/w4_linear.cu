@@ -193,7 +193,7 @@ __device__ __forceinline__ void copy16(void* dst, const void* src) {
 // tiles at a time) while the first weights are on their way; without it every
 // k tile waited for its activations.
 template <int NT, int R>
-__global__ void __launch_bounds__(kW4Threads, NT <= 2 ? 2 : 1) w4_kernel(const __grid_constant__ W4Args a) {
+__global__ void __launch_bounds__(kW4Threads, NT == 1 ? 3 : NT <= 2 ? 2 : 1) w4_kernel(const __grid_constant__ W4Args a) {
   extern __shared__ __align__(16) uint8_t w4_smem[];  // activations, then the sums [k warps][8 NT][rows + 4]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   cg::cluster_group cluster = cg::this_cluster();
@@ -556,11 +556,12 @@ int qtts_w4_linear(qtts_w4* w, int M, const uint16_t* x, int64_t x_stride, void*
   cudaError_t e;
   const cudaStream_t s = (cudaStream_t)stream;
   // Up to 8 rows: 16 weight rows a CTA, its warps along k (activations are few,
-  // weights spread over all SMs). More rows: 64 weight rows a CTA, so that fewer
-  // CTAs copy the activations. Clusters along k until the SMs have a CTA each and
-  // while every warp keeps two k tiles.
-  a.rw_log = M <= 8 ? 0 : 1;
-  const int ctas = M <= 8 ? w->RB : (w->RB + 3) / 4, kw = kW4Warps >> a.rw_log;
+  // weights spread over all SMs), 32 where that fills the SMs four times over
+  // (12288 x 2048: 6.7 us against 7.5). More rows: 64 weight rows a CTA, so that
+  // fewer CTAs copy the activations. Clusters along k until the SMs have a CTA
+  // each and while every warp keeps two k tiles.
+  a.rw_log = M <= 8 ? w->RB > 4 * w->G : 1;
+  const int ctas = M <= 8 ? w->RB >> a.rw_log : (w->RB + 3) / 4, kw = kW4Warps >> a.rw_log;
   while ((1 << a.s_log) < kW4MaxSplit && ctas << a.s_log < w->G && w->KT >= (4 * kw) << a.s_log) ++a.s_log;
   if (M <= 8) e = w4_launch<1, 1>(a, s);
   else e = M <= 16 ? w4_launch<2, 2>(a, s) : M <= 32 ? w4_launch<4, 2>(a, s) : w4_launch<8, 2>(a, s);

@@ -201,6 +201,18 @@ def test_single_tokens_over_ragged_contexts(d, nq, nkv):
         assert r.status() == (0, 0)
 
 
+@pytest.mark.parametrize("B,nq,nkv,top", [(300, 4, 2, 40), (300, 16, 2, 20), (150, 32, 2, 60), (40, 3, 3, 3), (1, 8, 8, 700)])
+def test_many_short_sessions(B, nq, nkv, top):
+    """More tiles than CTAs: a CTA goes through several, some of them shared with its neighbours."""
+    with Rig(B, top + 1, nq=nq, nkv=nkv, d=64) as r:
+        lens = [int(x) for x in r.rng.integers(0, top + 1, B)]
+        r.append([0] * B, [x + 1 for x in lens])
+        r.attend(lens, [1] * B, one=True)
+        some = [int(x) for x in r.rng.integers(0, 2, B)]
+        r.attend([x if s else -1 for x, s in zip(lens, some)], [1] * B)
+        assert r.status() == (0, 0)
+
+
 @pytest.mark.parametrize("n", [1023, 4000])
 def test_one_long_session_is_split_and_joined(n):
     with Rig(1, n + 1, nq=4, nkv=2) as r:
