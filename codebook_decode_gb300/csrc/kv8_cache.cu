@@ -20,6 +20,7 @@ constexpr int kMaxWarps = 16;
 // The rotation table: angles in double (a position of a long context times a
 // frequency loses its fraction in fp32), stored fp32.
 __global__ void rope_table_kernel(float* cs, float* sn, int max_context, int half, double theta) {
+  grid_dependency_wait();
   const int i = threadIdx.x;
   const double f = pow(theta, -(double)i / half);
   for (int p = blockIdx.x; p < max_context; p += gridDim.x) {
@@ -104,6 +105,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
     append_kernel(Kv8View c, Kv8Batch q, int touched, const uint16_t* __restrict__ k, int64_t k_stride,
                   const uint16_t* __restrict__ v, int64_t v_stride) {
   __shared__ __align__(16) float cs[kPage][D / 2], sn[kPage][D / 2];
+  grid_dependency_wait();
   const int b = blockIdx.x / touched;
   const PageTask t = page_task(c, q, b, blockIdx.x % touched);
   if (!t.valid) return;
@@ -240,6 +242,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
 template <int D>
 __global__ void __launch_bounds__(kMaxWarps * 32, 4)
     read_kernel(Kv8View c, Kv8Batch q, int touched, uint16_t* __restrict__ k, uint16_t* __restrict__ v) {
+  grid_dependency_wait();
   const int b = blockIdx.x / touched;
   const PageTask t = page_task(c, q, b, blockIdx.x % touched);
   const int lane = threadIdx.x & 31, task = blockIdx.y * (blockDim.x / 32) + threadIdx.x / 32;
@@ -353,6 +356,8 @@ cudaError_t launch(void (*kern)(P...), dim3 grid, int threads, cudaStream_t s, A
   lc.gridDim = grid;
   lc.blockDim = dim3(threads);
   lc.stream = s;
+  cudaLaunchAttribute at[1];
+  early_launch(lc, at);
   return cudaLaunchKernelEx(&lc, kern, (P)args...);
 }
 

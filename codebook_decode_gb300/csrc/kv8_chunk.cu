@@ -35,16 +35,21 @@ constexpr int kRows = 128, kKeys = 128, kPagesPerStep = kKeys / kPage;
 constexpr int kSoftmaxThreads = 256, kWidenThreads = 256;
 constexpr int kThreadsC = kSoftmaxThreads + kWidenThreads + 128;
 // registers of a thread: launched, then of the softmax, widening and issuing groups
-constexpr int kRegsLaunch = 96, kRegsSoftmax = 136, kRegsWiden = 80, kRegsIssue = 48;
+constexpr int kRegsLaunch = 96, kRegsSoftmax = 152, kRegsWiden = 64, kRegsIssue = 48;
 static_assert(kSoftmaxThreads * kRegsSoftmax + kWidenThreads * kRegsWiden + 128 * kRegsIssue <= kThreadsC * kRegsLaunch,
               "the groups share what the block was launched with");
-constexpr int kChunkTries = 1 << 20;
+constexpr int kChunkTries = 1 << 17;  // bound of each wait; a try sleeps up to about 10 us
 constexpr int kJoinSteps = 6;
 constexpr int kIssueWarp = (kSoftmaxThreads + kWidenThreads) / 32;
 
+// Bytes between the queries' core matrices along d: 16 more than their 128 rows
+// take, so that neighbouring lanes' stores fall on different banks (256 rows of
+// 128 dims leave no room for it).
+constexpr int lbo_q(int D, bool two) { return kRows * 16 + (D == 128 && two ? 0 : 16); }
+
 template <int D, bool TWO>
 struct ChunkSmem {
-  alignas(128) uint8_t q[TWO ? 2 : 1][kRows * D * 2];
+  alignas(128) uint8_t q[TWO ? 2 : 1][D / 8 * lbo_q(D, TWO)];
   uint8_t p[2][kRows * kKeys * 2];
   uint8_t k[2][kKeys * D * 2];
   uint8_t v[TWO ? 1 : 2][kKeys * D * 2];
@@ -115,17 +120,22 @@ struct Place {
 // weight of those before it.
 __device__ __forceinline__ int tiles_until(const Kv8Session& s, int rows_per_tile, bool whole, int limit, int& sum) {
   const int all = (s.n + rows_per_tile - 1) / rows_per_tile;
+  if (whole) return sum = min(all, limit);
   int t = 0, keys = s.L + rows_per_tile + kKeys - 1;
   sum = 0;
 #pragma unroll 1
   for (; t < all; ++t, keys += rows_per_tile) {
-    const int here = whole ? 1 : t + 1 < all ? keys / kKeys : (s.L + s.n + kKeys - 1) / kKeys;
+    const int here = t + 1 < all ? keys / kKeys : (s.L + s.n + kKeys - 1) / kKeys;
     if (sum + here > limit) break;
     sum += here;
   }
   return t;
 }
 
+template <int N>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_addr(dst)), "l"(src), "n"(N) : "memory");
+}
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
@@ -241,6 +251,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  grid_dependency_wait();
   if (warp == 0) {
     // Shares, and the place where this CTA's begins. Whole tiles where the most
     // that a CTA gets is not worse than an equal share and the cost of joining
@@ -322,9 +333,10 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
   }
   // bounded; once one wait has run out all others give up too
   auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (mbar_test(bar, parity)) return true;
     for (int tries = 0; tries < kChunkTries; ++tries) {
-      if (mbar_test(bar, parity)) return true;
-      if ((tries & 63) == 63 && *(volatile int*)&sm.failed) return false;
+      if (mbar_test_sleep(bar, parity, 10000)) return true;
+      if (*(volatile int*)&sm.failed) return false;
     }
     sm.failed = 1;
     set_err(a.c.err, QTTS_DEV_TIMEOUT);
@@ -332,7 +344,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
   };
   auto row_of = [&](int r) { return r * a.group_mul >> 16; };  // a tile row's query row
   // accumulators: S of group x at 128 x, O at 256 + 128 x
-  constexpr uint32_t kSbo = 128, kLboRow = kRows * 16, kLboV = D * 16;
+  constexpr uint32_t kLboQ = lbo_q(D, TWO), kSbo = 128, kLboRow = kRows * 16, kLboV = D * 16;
 
   if (warp >= kSoftmaxThreads / 32 && warp < kIssueWarp) {
     set_regs_down<kRegsWiden>();
@@ -392,10 +404,8 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
       load(0);
     }
     for (; left; ++j, --left) {
-      if ((j & 15) == 0) {
-        if (j) ids = ids_next;
-        ids_next = fetch_ids((j >> 4) + 1);
-      }
+      if ((j & 15) == 0 && j) ids = ids_next;
+      if ((j & 15) == 8) ids_next = fetch_ids((j >> 4) + 1);
       const int s = j & 1;
       if (!is_v) {
         if (j >= 2) ok = wait(&sm.kdone[s], ((j >> 1) - 1) & 1);
@@ -454,11 +464,12 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
         const int s = jj & 1;
         if (!(ok = wait(&sm.kfull[s], (jj >> 1) & 1))) return;
         tc_fence_after();
-        const uint32_t qa = smem_addr(sm.q[TWO ? x : 0]), ka = smem_addr(sm.k[s]);
+        // a descriptor's low bits are the address in 16-byte units: steps along k add to it
+        uint64_t qd = tc_smem_desc(smem_addr(sm.q[TWO ? x : 0]), kLboQ, kSbo);
+        uint64_t kd = tc_smem_desc(smem_addr(sm.k[s]), kLboRow, kSbo);
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          tc_mma(tmem + 128 * x, tc_smem_desc(qa + ks * 2 * kLboRow, kLboRow, kSbo),
-                 tc_smem_desc(ka + ks * 2 * kLboRow, kLboRow, kSbo), idS, ks > 0);
+        for (int ks = 0; ks < D / 16; ++ks, qd += 2 * kLboQ / 16, kd += 2 * kLboRow / 16)
+          tc_mma(tmem + 128 * x, qd, kd, idS, ks > 0);
         tc_commit(&sm.sdone[x]);
         mbar_arrive(&sm.sdone[x]);
         if (last) tc_commit(&sm.kdone[s]);
@@ -469,11 +480,10 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
         if (!ok) return;
         ++n[x];
         tc_fence_after();
-        const uint32_t pa = smem_addr(sm.p[x]), va = smem_addr(sm.v[vs]);
+        uint64_t pd = tc_smem_desc(smem_addr(sm.p[x]), kLboRow, kSbo), vd = tc_smem_desc(smem_addr(sm.v[vs]), kLboV, kSbo);
 #pragma unroll
-        for (int ks = 0; ks < kKeys / 16; ++ks)
-          tc_mma(tmem + 256 + 128 * x, tc_smem_desc(pa + ks * 2 * kLboRow, kLboRow, kSbo),
-                 tc_smem_desc(va + ks * 2 * kLboV, kLboV, kSbo), idO, !first || ks > 0);
+        for (int ks = 0; ks < kKeys / 16; ++ks, pd += 2 * kLboRow / 16, vd += 2 * kLboV / 16)
+          tc_mma(tmem + 256 + 128 * x, pd, vd, idO, !first || ks > 0);
         tc_commit(&sm.pvdone[x]);
         if (last) tc_commit(&sm.vdone[vs]);
       };
@@ -524,90 +534,80 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
       const int row0 = w.t * a.rows_per_tile, rows = min(a.rows_per_tile, w.s.n - row0), cols = rows * a.group;
       const int pos = w.s.L + row0 + min(row_of(TWO ? tid : row), rows - 1);  // last position that this row sees
       const bool active = !TWO || x == 0 || cols > kRows;
-      // The tile's queries, rotated, into shared memory: a warp takes 8 rows at
-      // a time, lane (r, t) of it 8 dims of row r in every 32, with the partner
-      // dims D/2 further. Scaled by the power of two of the row's largest
-      // magnitude (before the rotation, which can grow it by sqrt 2: half has room).
-      constexpr int kWarpRows = TWO ? 32 : 16;
-      auto load_rows = [&](int r0, uint2 (&raw)[D / 32][2], float4 (&cs)[D / 64][2], float4 (&sn)[D / 64][2]) {
-        const int rr = r0 + (lane & 7), t = lane >> 3, q1 = row_of(rr);
-        const uint16_t* src = a.qp + (int64_t)(w.s.r0 + row0 + q1) * a.q_stride +
-                              (size_t)(w.h * a.group + rr - q1 * a.group) * D + 8 * t;
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e)
-#pragma unroll
-          for (int f = 0; f < 2; ++f) {
-            raw[e][f] = make_uint2(0u, 0u);
-            if (rr < cols) raw[e][f] = *(const uint2*)(src + 32 * e + 4 * f);
-          }
-        if (a.c.rope_cos) {
-          const size_t at = (size_t)(w.s.L + row0 + min(q1, rows - 1)) * (D / 2) + 8 * t;
-#pragma unroll
-          for (int e = 0; e < D / 64; ++e)
-#pragma unroll
-            for (int f = 0; f < 2; ++f) {
-              cs[e][f] = *(const float4*)(a.c.rope_cos + at + 32 * e + 4 * f);
-              sn[e][f] = *(const float4*)(a.c.rope_sin + at + 32 * e + 4 * f);
-            }
+      // The tile's queries, rotated, into shared memory. They and their rotations
+      // are copied to the weights' place first, up to 128 rows at a time, all
+      // copies in flight at once (loaded into registers they took a memory
+      // latency for every few rows). A thread then takes 4 dims of a row and
+      // their partners D/2 further, D/8 lanes a row. Scaled by the power of two
+      // of the row's largest magnitude (before the rotation, which can grow it by
+      // sqrt 2: half has room).
+      constexpr int kQuads = D / 8, kRowsOnce = kSoftmaxThreads / kQuads;
+      uint8_t* raw = sm.p[0];                    // [128][D] bf16
+      uint8_t* turn = sm.p[0] + kRows * D * 2;   // [tokens][D / 2 cosines, D / 2 sines]; tokens x D x 4 <= 128 x D x 2
+      const int pass_tokens = a.group > 1 ? kRows * a.group_mul >> 16 : kRows / 2;
+#pragma unroll 1
+      for (int tok = 0; tok < rows; tok += pass_tokens) {
+        const int tokens = min(pass_tokens, rows - tok), first = tok * a.group, count = tokens * a.group;
+        for (int i = tid; i < count * (D / 4); i += kSoftmaxThreads) {
+          const int r = first + i / (D / 4), at = i % (D / 4) * 4, rq = row_of(r);
+          copy_async<8>(raw + i * 8, a.qp + (int64_t)(w.s.r0 + row0 + rq) * a.q_stride + (size_t)(w.h * a.group + r - rq * a.group) * D + at);
         }
-      };
-      auto put_rows = [&](int r0, uint2 (&raw)[D / 32][2], float4 (&cs)[D / 64][2], float4 (&sn)[D / 64][2]) {
-        const int rr = r0 + (lane & 7), t = lane >> 3;
-        uint32_t mag = 0;
+        if (a.c.rope_cos)
+          for (int i = tid; i < tokens * (D / 4); i += kSoftmaxThreads) {
+            const int at = i % (D / 8) * 4;
+            const float* src = i / (D / 8) & 1 ? a.c.rope_sin : a.c.rope_cos;
+            copy_async<16>(turn + i * 16, src + (size_t)(w.s.L + row0 + tok + i / (D / 4)) * (D / 2) + at);
+          }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        softmax_sync();
+        const int quad = tid % kQuads * 4;
+#pragma unroll 2
+        for (int rl = tid / kQuads; rl < (count + kRowsOnce - 1) / kRowsOnce * kRowsOnce; rl += kRowsOnce) {
+          const int r = first + rl;
+          uint2 lo2 = make_uint2(0u, 0u), hi2 = lo2;
+          if (rl < count) {
+            lo2 = *(const uint2*)(raw + (rl * D + quad) * 2);
+            hi2 = *(const uint2*)(raw + (rl * D + D / 2 + quad) * 2);
+          }
+          uint32_t mag = __vmaxu2(__vmaxu2(lo2.x & 0x7fff7fffu, lo2.y & 0x7fff7fffu), __vmaxu2(hi2.x & 0x7fff7fffu, hi2.y & 0x7fff7fffu));
+          mag = max(mag & 0xffffu, mag >> 16);
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e)
+          for (int o = 1; o < kQuads; o <<= 1) mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, o));
+          const uint32_t ex = min(max(mag << 16 & 0x7f800000u, 1u << 23), 253u << 23);
+          const float inv = __uint_as_float((254u << 23) - ex) * a.q_sign;
+          const float lo[4] = {bf2f(lo2.x & 0xffffu), __uint_as_float(lo2.x & 0xffff0000u), bf2f(lo2.y & 0xffffu), __uint_as_float(lo2.y & 0xffff0000u)};
+          const float hi[4] = {bf2f(hi2.x & 0xffffu), __uint_as_float(hi2.x & 0xffff0000u), bf2f(hi2.y & 0xffffu), __uint_as_float(hi2.y & 0xffff0000u)};
+          float u[4], v[4];
+          const float* tr = (const float*)turn + (row_of(r) - tok) * D + quad;
 #pragma unroll
-          for (int f = 0; f < 2; ++f) mag = __vmaxu2(mag, __vmaxu2(raw[e][f].x & 0x7fff7fffu, raw[e][f].y & 0x7fff7fffu));
-        mag = max(mag & 0xffffu, mag >> 16);
-        mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 8));
-        mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 16));
-        const uint32_t ex = min(max(mag << 16 & 0x7f800000u, 1u << 23), 253u << 23);
-        const float inv = __uint_as_float((254u << 23) - ex) * a.q_sign;
-        float sum = 0.f;  // of the row's halves
-        uint8_t* base = sm.q[TWO ? rr >> 7 : 0] + (rr & 127) / 8 * 128 + rr % 8 * 16;
-#pragma unroll
-        for (int e = 0; e < D / 64; ++e) {
-          const uint2 l0 = raw[e][0], l1 = raw[e][1], h0 = raw[e + D / 64][0], h1 = raw[e + D / 64][1];
-          const uint32_t wl[4] = {l0.x, l0.y, l1.x, l1.y}, wh[4] = {h0.x, h0.y, h1.x, h1.y};
-          const float cv[8] = {cs[e][0].x, cs[e][0].y, cs[e][0].z, cs[e][0].w, cs[e][1].x, cs[e][1].y, cs[e][1].z, cs[e][1].w};
-          const float sv[8] = {sn[e][0].x, sn[e][0].y, sn[e][0].z, sn[e][0].w, sn[e][1].x, sn[e][1].y, sn[e][1].z, sn[e][1].w};
-          float u[8], v[8];
-#pragma unroll
-          for (int f = 0; f < 8; ++f) {
-            const float p = (f & 1 ? __uint_as_float(wl[f / 2] & 0xffff0000u) : bf2f(wl[f / 2] & 0xffffu)) * inv;
-            const float q = (f & 1 ? __uint_as_float(wh[f / 2] & 0xffff0000u) : bf2f(wh[f / 2] & 0xffffu)) * inv;
+          for (int f = 0; f < 4; ++f) {
+            const float p = lo[f] * inv, q = hi[f] * inv;
             u[f] = p;
             v[f] = q;
-            if (a.c.rope_cos) {
-              u[f] = p * cv[f] - q * sv[f];
-              v[f] = q * cv[f] + p * sv[f];
+            if (a.c.rope_cos && rl < count) {
+              const float cs = tr[f], sn = tr[D / 2 + f];
+              u[f] = p * cs - q * sn;
+              v[f] = q * cs + p * sn;
             }
           }
-          uint8_t* dst = base + (4 * e + t) * kLboRow;
-          const uint32_t hu[8] = {half2_bits(u[0], u[1]), half2_bits(u[2], u[3]), half2_bits(u[4], u[5]), half2_bits(u[6], u[7]),
-                                  half2_bits(v[0], v[1]), half2_bits(v[2], v[3]), half2_bits(v[4], v[5]), half2_bits(v[6], v[7])};
+          const uint32_t hu[4] = {half2_bits(u[0], u[1]), half2_bits(u[2], u[3]), half2_bits(v[0], v[1]), half2_bits(v[2], v[3])};
+          float sum = 0.f;  // of the row's halves
 #pragma unroll
-          for (int f = 0; f < 8; ++f) {
+          for (int f = 0; f < 4; ++f) {
             const float2 y = __half22float2(*(const __half2*)&hu[f]);
             sum += y.x + y.y;
           }
-          *(uint4*)dst = make_uint4(hu[0], hu[1], hu[2], hu[3]);
-          *(uint4*)(dst + D / 16 * kLboRow) = make_uint4(hu[4], hu[5], hu[6], hu[7]);
+#pragma unroll
+          for (int o = 1; o < kQuads; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          if (rl < count) {
+            uint8_t* dst = sm.q[TWO ? r >> 7 : 0] + quad / 8 * kLboQ + (r & 127) / 8 * 128 + r % 8 * 16 + (quad & 4) * 2;
+            *(uint2*)dst = make_uint2(hu[0], hu[1]);
+            *(uint2*)(dst + D / 16 * kLboQ) = make_uint2(hu[2], hu[3]);
+            if (quad == 0) sm.ml[TWO ? r >> 7 : 1][r & 127] = make_float2(__uint_as_float(ex) * a.scale_log2, 1152.f * sum);
+          }
         }
-        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-        if (t == 0) sm.ml[TWO ? rr >> 7 : 1][rr & 127] = make_float2(__uint_as_float(ex) * a.scale_log2, 1152.f * sum);
-      };
-#pragma unroll 1
-      for (int r0 = kWarpRows * warp; r0 < min(kWarpRows * (warp + 1), cols); r0 += 16) {
-        uint2 raw[2][D / 32][2];
-        float4 c[2][D / 64][2], s[2][D / 64][2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) load_rows(r0 + 8 * i, raw[i], c[i], s[i]);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) put_rows(r0 + 8 * i, raw[i], c[i], s[i]);
+        softmax_sync();  // before the next rows or the first weights take the place
       }
-      softmax_sync();
       const float cf = sm.ml[TWO ? x : 1][row].x, surplus = sm.ml[TWO ? x : 1][row].y;
       fence_async_shared();
       tc_fence_before();  // the last tile's accumulators have been read
@@ -849,6 +849,8 @@ cudaError_t launch_chunk(const ChunkArgs& a, int sms, cudaStream_t s) {
   lc.blockDim = dim3(kThreadsC);
   lc.dynamicSmemBytes = sizeof(ChunkSmem<D, TWO>);
   lc.stream = s;
+  cudaLaunchAttribute at[1];
+  early_launch(lc, at);
   return cudaLaunchKernelEx(&lc, chunk_kernel<D, TWO>, a);
 }
 template <int D, bool TWO>

@@ -238,6 +238,7 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 3 : NT <= 2 ? 2 : 1) w4_
     };
 #pragma unroll
     for (int i = 0; i < P; ++i) fetch(i, k0 + i);
+    if (c0 == t0) grid_dependency_wait();  // weights are there since they were loaded; activations may be on their way
     // activations: 16 bytes are 8 k; beyond K zeros (the codes there are 0)
     const int per_row = n * (kW4K / 8), have = min(per_row, a.K / 8 - c0 * (kW4K / 8));
     if (c0 > t0) __syncthreads();  // the last chunk has been read
@@ -369,12 +370,12 @@ cudaError_t w4_launch(W4Args a, cudaStream_t s) {
   lc.blockDim = dim3(kW4Threads);
   lc.dynamicSmemBytes = std::max((size_t)a.M * (a.chunk * kW4K * 2 + 64), (size_t)kw * 8 * NT * (cta_rows + 4) * sizeof(float));
   lc.stream = s;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = S;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  lc.attrs = at;
   lc.numAttrs = 1;
+  early_launch(lc, at);
   return cudaLaunchKernelEx(&lc, w4_kernel<NT, R>, a);
 }
 
