@@ -35,7 +35,7 @@ constexpr int kRows = 128, kKeys = 128, kPagesPerStep = kKeys / kPage;
 constexpr int kSoftmaxThreads = 256, kWidenThreads = 256;
 constexpr int kThreadsC = kSoftmaxThreads + kWidenThreads + 128;
 // registers of a thread: launched, then of the softmax, widening and issuing groups
-constexpr int kRegsLaunch = 96, kRegsSoftmax = 152, kRegsWiden = 64, kRegsIssue = 48;
+constexpr int kRegsLaunch = 96, kRegsSoftmax = 144, kRegsWiden = 64, kRegsIssue = 64;
 static_assert(kSoftmaxThreads * kRegsSoftmax + kWidenThreads * kRegsWiden + 128 * kRegsIssue <= kThreadsC * kRegsLaunch,
               "the groups share what the block was launched with");
 constexpr int kChunkTries = 1 << 17;  // bound of each wait; a try sleeps up to about 10 us
@@ -474,11 +474,14 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
         mbar_arrive(&sm.sdone[x]);
         if (last) tc_commit(&sm.kdone[s]);
       };
+      auto weights_there = [&](int x) {  // group x has read its scores and written its weights
+        ok = wait(&sm.pfull[x], n[x] & 1);
+        ++n[x];
+        return ok;
+      };
       auto values = [&](int jj, int x, bool first, bool last) {  // group x's second product of step jj
         const int vs = TWO ? 0 : jj & 1;
-        ok = wait(&sm.pfull[x], n[x] & 1) && wait(&sm.vfull[vs], TWO ? jj & 1 : (jj >> 1) & 1);
-        if (!ok) return;
-        ++n[x];
+        if (!(ok = wait(&sm.vfull[vs], TWO ? jj & 1 : (jj >> 1) & 1))) return;
         tc_fence_after();
         uint64_t pd = tc_smem_desc(smem_addr(sm.p[x]), kLboRow, kSbo), vd = tc_smem_desc(smem_addr(sm.v[vs]), kLboV, kSbo);
 #pragma unroll
@@ -498,15 +501,16 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
           for (; j < j1 && ok; ++j)
 #pragma unroll 1
             for (int x = 0; x <= both && ok; ++x) {
-              values(j, x, j == j0, x == both);
-              if (ok && j + 1 < j1) scores(j + 1, x, x == both);
+              // the group's next scores first: it waits for them, not for the values
+              if (weights_there(x) && j + 1 < j1) scores(j + 1, x, x == both);
+              if (ok) values(j, x, j == j0, x == both);
             }
         } else {
 #pragma unroll 1
           for (int i = 0; i < min(cnt, 2) && ok; ++i) scores(j + i, (j + i) & 1, true);
           for (; j < j1 && ok; ++j) {
-            values(j, j & 1, j - j0 < 2, true);
-            if (ok && j + 2 < j1) scores(j + 2, j & 1, true);
+            if (weights_there(j & 1) && j + 2 < j1) scores(j + 2, j & 1, true);
+            if (ok) values(j, j & 1, j - j0 < 2, true);
           }
         }
         left -= cnt;
