@@ -31,9 +31,10 @@ __global__ void rope_table_kernel(float* cs, float* sn, int max_context, int hal
   }
 }
 
-__device__ __forceinline__ float4 bf4(uint2 v) {
-  return make_float4(bf2f(v.x & 0xffffu), __uint_as_float(v.x & 0xffff0000u), bf2f(v.y & 0xffffu),
-                     __uint_as_float(v.y & 0xffff0000u));
+// Four bf16 as two pairs of fp32.
+__device__ __forceinline__ void bf4(uint2 v, uint64_t& a, uint64_t& b) {
+  a = pack2(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u));
+  b = pack2(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
 }
 // largest magnitude of the three, NaN if one is
 __device__ __forceinline__ float max_abs(float a, float b, float c) {
@@ -41,15 +42,26 @@ __device__ __forceinline__ float max_abs(float a, float b, float c) {
   asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
+__device__ __forceinline__ float max_abs(float m, uint64_t a) {
+  const float2 f = unpack2(a);
+  return max_abs(m, f.x, f.y);
+}
 // Rounding to an integer by adding 1.5 * 2^23 (half-even, like the product
 // before it in binary32); with 128 on top the low byte is the stored code. No
 // clamp: x * inv is at most 127 (1 + 2^-22).
-__device__ __forceinline__ uint32_t code_bits(float x, float inv) {
-  return __float_as_uint(__fadd_rn(__fmul_rn(x, inv), 12583040.f));
+// The products stay scalar: the paired multiply and add were fused into one rounding.
+__device__ __forceinline__ uint64_t code_bits(uint64_t x, float inv) {
+  const float2 f = unpack2(x);
+  return add2(pack2(__fmul_rn(f.x, inv), __fmul_rn(f.y, inv)), pack2(12583040.f, 12583040.f));
 }
-__device__ __forceinline__ uint32_t codes4(float x, float y, float z, float w, float inv) {
-  return __byte_perm(__byte_perm(code_bits(x, inv), code_bits(y, inv), 0x0040),
-                     __byte_perm(code_bits(z, inv), code_bits(w, inv), 0x0040), 0x5410);
+// the low bytes of four
+__device__ __forceinline__ uint32_t bytes4(float x, float y, float z, float w) {
+  return __byte_perm(__byte_perm(__float_as_uint(x), __float_as_uint(y), 0x0040),
+                     __byte_perm(__float_as_uint(z), __float_as_uint(w), 0x0040), 0x5410);
+}
+__device__ __forceinline__ uint32_t codes4(uint64_t a, uint64_t b, float inv) {
+  const float2 x = unpack2(code_bits(a, inv)), y = unpack2(code_bits(b, inv));
+  return bytes4(x.x, x.y, y.x, y.y);
 }
 // byte i of c as its code: the byte under the exponent of 2^23, minus 2^23 + 128
 __device__ __forceinline__ float code_value(uint32_t c, int i) {
@@ -57,7 +69,7 @@ __device__ __forceinline__ float code_value(uint32_t c, int i) {
 }
 // codes at scale s_old as codes at a larger scale, r = s_old / s
 __device__ __forceinline__ uint32_t rescale4(uint32_t c, float r) {
-  return codes4(code_value(c, 0), code_value(c, 1), code_value(c, 2), code_value(c, 3), r);
+  return codes4(pack2(code_value(c, 0), code_value(c, 1)), pack2(code_value(c, 2), code_value(c, 3)), r);
 }
 
 // The page that a CTA works on and its new rows; valid: there are any.
@@ -104,7 +116,7 @@ template <int D>
 __global__ void __launch_bounds__(kMaxWarps * 32, 2)
     append_kernel(Kv8View c, Kv8Batch q, int touched, const uint16_t* __restrict__ k, int64_t k_stride,
                   const uint16_t* __restrict__ v, int64_t v_stride) {
-  __shared__ __align__(16) float cs[kPage][D / 2], sn[kPage][D / 2];
+  __shared__ __align__(16) float cs[kPage][D / 2], sn[kPage][D / 2], neg[kPage][D / 2];  // neg: -sn
   grid_dependency_wait();
   const int b = blockIdx.x / touched;
   const PageTask t = page_task(c, q, b, blockIdx.x % touched);
@@ -151,7 +163,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
     const float4* s4 = (const float4*)(c.rope_sin + (size_t)t.pos0 * (D / 2));
     for (int i = threadIdx.x; i < n4; i += blockDim.x) {
       ((float4*)cs[t.first])[i] = c4[i];
-      ((float4*)sn[t.first])[i] = s4[i];
+      const float4 v = s4[i];
+      ((float4*)sn[t.first])[i] = v;
+      ((float4*)neg[t.first])[i] = make_float4(-v.x, -v.y, -v.z, -v.w);
     }
     __syncthreads();
   }
@@ -164,38 +178,62 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
   const float s_old = t.first > 0 ? *sp : 0.f;
 
   if (which == 0) {
-    float4 a[PASSES], p4[PASSES];
-    float mx = 0.f;
-#pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
+    // Rotated twice, for the magnitude and for the codes: kept, the values would
+    // not fit the registers that two CTAs of 16 warps leave.
+    auto rotated = [&](int p, uint64_t (&x)[2], uint64_t (&y)[2]) {
       const int slot = p * TPP + tk;
-      float4 x = bf4(raw[2 * p]), y = bf4(raw[2 * p + 1]);
-      if (c.rope_cos && fresh_slot(slot)) {
-        const float4 f = *(const float4*)&cs[slot][i4], g = *(const float4*)&sn[slot][i4];
-        const float4 u = x, w = y;
-        x = make_float4(u.x * f.x - w.x * g.x, u.y * f.y - w.y * g.y, u.z * f.z - w.z * g.z, u.w * f.w - w.w * g.w);
-        y = make_float4(w.x * f.x + u.x * g.x, w.y * f.y + u.y * g.y, w.z * f.z + u.z * g.z, w.w * f.w + u.w * g.w);
+      bf4(raw[2 * p], x[0], x[1]);
+      bf4(raw[2 * p + 1], y[0], y[1]);
+      if (c.rope_cos) {
+        const ulonglong2 f = *(const ulonglong2*)&cs[slot][i4], g = *(const ulonglong2*)&sn[slot][i4],
+                         h = *(const ulonglong2*)&neg[slot][i4];
+        const uint64_t u0 = x[0], u1 = x[1];
+        x[0] = fma2(u0, f.x, mul2(y[0], h.x));
+        x[1] = fma2(u1, f.y, mul2(y[1], h.y));
+        y[0] = fma2(y[0], f.x, mul2(u0, g.x));
+        y[1] = fma2(y[1], f.y, mul2(u1, g.y));
       }
-      a[p] = x;
-      p4[p] = y;
-      mx = max_abs(max_abs(mx, x.x, x.y), x.z, x.w);
-      mx = max_abs(max_abs(mx, y.x, y.y), y.z, y.w);
-    }
-    const float s = new_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)), s_old);
-    const float inv = s > 0.f ? 1.f / s : 0.f;
-    const bool grown = s > s_old && s_old > 0.f;
-    const float r = grown ? s_old / s : 0.f;
+    };
     // dims x of token `slot` stand at [x / 64][slot][x % 64]
-    auto at = [&](int slot, int x) { return (uint32_t*)(codes + x / 64 * 1024 + slot * 64 + x % 64); };
+    uint8_t* dst = codes + i4 / 64 * 1024 + i4 % 64 + tk * 64;
+    constexpr int kPartner = D == 128 ? 1024 : 32;
+    auto block = [&](auto fresh) {
+      float mx = 0.f;
 #pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-      const int slot = p * TPP + tk;
-      if (fresh_slot(slot)) {
-        *at(slot, i4) = codes4(a[p].x, a[p].y, a[p].z, a[p].w, inv);
-        *at(slot, i4 + D / 2) = codes4(p4[p].x, p4[p].y, p4[p].z, p4[p].w, inv);
-      } else if (grown && slot < t.first) {
-        *at(slot, i4) = rescale4(*at(slot, i4), r);
-        *at(slot, i4 + D / 2) = rescale4(*at(slot, i4 + D / 2), r);
+      for (int p = 0; p < PASSES; ++p)
+        if (fresh(p * TPP + tk)) {
+          uint64_t x[2], y[2];
+          rotated(p, x, y);
+          mx = max_abs(max_abs(max_abs(max_abs(mx, x[0]), x[1]), y[0]), y[1]);
+        }
+      const float s = new_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)), s_old);
+      const float inv = s > 0.f ? 1.f / s : 0.f;
+#pragma unroll
+      for (int p = 0; p < WORDS; ++p) asm volatile("" : "+r"(raw[p].x), "+r"(raw[p].y));  // or the compiler keeps them
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p)
+        if (fresh(p * TPP + tk)) {
+          uint64_t x[2], y[2];
+          rotated(p, x, y);
+          *(uint32_t*)(dst + p * TPP * 64) = codes4(x[0], x[1], inv);
+          *(uint32_t*)(dst + p * TPP * 64 + kPartner) = codes4(y[0], y[1], inv);
+        }
+      return s;
+    };
+    float s;
+    if (all) {
+      s = block([](int) { return true; });
+    } else {
+      s = block([&](int slot) { return slot >= t.first && slot < t.last; });
+      if (s > s_old && s_old > 0.f) {  // the codes of the tokens before follow
+        const float r = s_old / s;
+#pragma unroll 1
+        for (int p = 0; p * TPP + tk < t.first; ++p) {
+          uint32_t* w = (uint32_t*)(dst + p * TPP * 64);
+          uint32_t* v = (uint32_t*)(dst + p * TPP * 64 + kPartner);
+          *w = rescale4(*w, r);
+          *v = rescale4(*v, r);
+        }
       }
     }
     __syncwarp();  // every lane has read the old scale
@@ -212,10 +250,17 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
       uint4* dst = (uint4*)(codes + x4 * 64 + (t0 + n) * 16);
-      const float4 y0 = bf4(raw[4 * n]), y1 = bf4(raw[4 * n + 1]), y2 = bf4(raw[4 * n + 2]), y3 = bf4(raw[4 * n + 3]);
+      float2 q[4][2];  // token j's four codes
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint64_t a, b;
+        bf4(raw[4 * n + j], a, b);
+        q[j][0] = unpack2(code_bits(a, inv));
+        q[j][1] = unpack2(code_bits(b, inv));
+      }
       // word i: dim 4 x4 + i, byte j: token j of the quad
-      uint4 o = make_uint4(codes4(y0.x, y1.x, y2.x, y3.x, inv), codes4(y0.y, y1.y, y2.y, y3.y, inv),
-                           codes4(y0.z, y1.z, y2.z, y3.z, inv), codes4(y0.w, y1.w, y2.w, y3.w, inv));
+      uint4 o = make_uint4(bytes4(q[0][0].x, q[1][0].x, q[2][0].x, q[3][0].x), bytes4(q[0][0].y, q[1][0].y, q[2][0].y, q[3][0].y),
+                           bytes4(q[0][1].x, q[1][1].x, q[2][1].x, q[3][1].x), bytes4(q[0][1].y, q[1][1].y, q[2][1].y, q[3][1].y));
       if (!all) {
         uint4 old = *dst;
         uint32_t fresh = 0, before = 0;  // byte masks of the new tokens, of those before them
