@@ -28,7 +28,13 @@ __device__ __forceinline__ uint64_t global_timer_ns() {
   return t;
 }
 __device__ __forceinline__ int read_err(const int* e) { return *(const volatile int*)e; }
-__device__ __forceinline__ void set_err(int* e, int code) { atomicCAS(e, 0, code); }
+__host__ __device__ __forceinline__ void set_err(int* e, int code) {
+#ifdef __CUDA_ARCH__
+  atomicCAS(e, 0, code);
+#else
+  if (!*e) *e = code;
+#endif
+}
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count) : "memory");

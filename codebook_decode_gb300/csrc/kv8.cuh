@@ -70,7 +70,7 @@ struct Kv8Session {
 // The session's rows and length, checked: what does not fit its block table,
 // the rotation table or the call's own limits sets the error word and is
 // skipped. A negative kv_len marks an inactive session.
-__device__ __forceinline__ Kv8Session kv8_session(const Kv8Batch& q, int b, int max_context, int* err) {
+__host__ __device__ __forceinline__ Kv8Session kv8_session(const Kv8Batch& q, int b, int max_context, int* err) {
   Kv8Session s;
   s.r0 = q.row_start ? q.row_start[b] : b;
   const int r1 = q.row_start ? q.row_start[b + 1] : b + 1;
@@ -94,12 +94,14 @@ __device__ __forceinline__ Kv8Session kv8_session(const Kv8Batch& q, int b, int 
 }
 
 cudaError_t kv8_chunk_setup(int d);
+bool kv8_chunk_fits(const Kv8View& v, const Kv8Batch& q, int group, long long pages);
 size_t kv8_chunk_workspace(int d, int sms);
 cudaError_t kv8_chunk(const Kv8View& v, const Kv8Batch& q, int d, int group, int sms, const uint16_t* qp,
                       int64_t q_stride, float scale, uint16_t* out, int64_t out_stride, unsigned* arrived, float* part,
                       cudaStream_t s);
 cudaError_t kv8_attention_setup(int d);
 size_t kv8_attention_workspace(int d, int sms);
+bool kv8_attention_fits(const Kv8View& v, const Kv8Batch& q, int group);
 cudaError_t kv8_attention(const Kv8View& v, const Kv8Batch& q, int d, int group, int sms, const uint16_t* qp,
                           int64_t q_stride, float scale, uint16_t* out, int64_t out_stride, void* work, cudaStream_t s);
 

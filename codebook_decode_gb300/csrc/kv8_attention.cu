@@ -722,11 +722,16 @@ size_t kv8_attention_workspace(int d, int sms) {
   return ctas * sizeof(unsigned) + std::max(2 * ctas * kMaxCols * (d + 4) * sizeof(float), kv8_chunk_workspace(d, sms));
 }
 
+// Places in the work are 32-bit: pages of all sessions and kv heads, or key
+// steps of all tiles. What a call can need at most, from its sizes.
+bool kv8_attention_fits(const Kv8View& v, const Kv8Batch& q, int group) {
+  const long long pages = std::min((long long)q.bt_stride, v.max_context / kPage + 1ll);
+  if ((long long)q.max_new * group <= kMaxCols) return q.B * pages * v.nkv < (1ll << 31);
+  return kv8_chunk_fits(v, q, group, pages);
+}
+
 cudaError_t kv8_attention(const Kv8View& v, const Kv8Batch& q, int d, int group, int sms, const uint16_t* qp,
                           int64_t q_stride, float scale, uint16_t* out, int64_t out_stride, void* work, cudaStream_t s) {
-  // places in the units are 32-bit
-  const long long tiles = (q.max_new + 0ll) * group / 8 + 1, pages = std::min(q.bt_stride, v.max_context / kPage + 1);
-  if (q.B * pages * v.nkv >= (1ll << 31) / std::max(tiles, 1ll)) return cudaErrorInvalidValue;
   // the fewest n-tiles that hold every session's columns; more rows go in tiles of 32 columns
   const long long cols = (long long)q.max_new * group;
   float* part = (float*)((char*)work + 2 * (size_t)sms * sizeof(unsigned));

@@ -343,19 +343,6 @@ int fail(qtts_kv8* c, int code, const char* fmt, ...) {
   return code;
 }
 
-// The caller's current device is put back on every path out.
-struct DeviceGuard {
-  int prev = -1, dev;
-  bool ok;
-  explicit DeviceGuard(int d) : dev(d) {
-    if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
-    ok = prev == d || cudaSetDevice(d) == cudaSuccess;
-  }
-  ~DeviceGuard() {
-    if (prev >= 0 && prev != dev) cudaSetDevice(prev);
-  }
-};
-
 const char* config_fault(const qtts_kv8_config& c) {
   if (c.n_layers <= 0 || c.n_q_heads <= 0 || c.n_kv_heads <= 0 || c.pool_pages <= 0) return "sizes must be positive";
   if (c.head_dim != 64 && c.head_dim != 128) return "head_dim must be 64 or 128";
@@ -578,6 +565,8 @@ int qtts_kv8_attention(qtts_kv8* c, int layer, int B, int n_rows, int max_new, c
     return fail(c, QTTS_E_INVALID, "qtts_kv8_attention: workspace must be given and 16-byte aligned");
   if (!std::isfinite(scale)) return fail(c, QTTS_E_INVALID, "qtts_kv8_attention: scale must be finite");
   if (rc) return QTTS_OK;
+  if (!kv8_attention_fits(view(c, layer), qb, f.n_q_heads / f.n_kv_heads))
+    return fail(c, QTTS_E_INVALID, "qtts_kv8_attention: too much work for one call, split the batch");
   DeviceGuard g(c->device);
   if (!g.ok) return fail(c, QTTS_E_CUDA, "cudaSetDevice failed");
   const cudaError_t e = kv8_attention(view(c, layer), qb, f.head_dim, f.n_q_heads / f.n_kv_heads, c->G, q, q_stride,

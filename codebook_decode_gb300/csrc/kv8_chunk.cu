@@ -851,6 +851,11 @@ cudaError_t kv8_chunk_setup(int d) {
 
 size_t kv8_chunk_workspace(int d, int sms) { return 2 * (size_t)sms * 2 * kRows * (d + 4) * sizeof(float); }
 
+bool kv8_chunk_fits(const Kv8View& v, const Kv8Batch& q, int group, long long pages) {
+  const long long tiles = q.n_rows / (kRows / group) + q.B, steps = pages * kPage / kKeys + 2;
+  return tiles * v.nkv < (1ll << 31) / steps;
+}
+
 cudaError_t kv8_chunk(const Kv8View& v, const Kv8Batch& q, int d, int group, int sms, const uint16_t* qp,
                       int64_t q_stride, float scale, uint16_t* out, int64_t out_stride, unsigned* arrived, float* part,
                       cudaStream_t s) {

@@ -263,6 +263,19 @@ cudaError_t pf_chunk(const PfCtx& c, int B, int P, const qtts_session* sess, con
 cudaError_t pf_talker_step(const PfCtx& c, int B, const qtts_session* sess, const int32_t* bt, int bt_stride,
                            const uint16_t* in_embeds, uint64_t* x_words, uint32_t tag, cudaStream_t s);
 
+// The caller's current device is put back on every path out.
+struct DeviceGuard {
+  int prev = -1, dev;
+  bool ok;
+  explicit DeviceGuard(int d) : dev(d) {
+    if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
+    ok = prev == d || cudaSetDevice(d) == cudaSuccess;
+  }
+  ~DeviceGuard() {
+    if (prev >= 0 && prev != dev) cudaSetDevice(prev);
+  }
+};
+
 // qtts_api.cu: model internals for other translation units
 struct KvLayout {
   int device;

@@ -389,18 +389,6 @@ int fail(qtts_w4* w, int code, const char* fmt, ...) {
   return code;
 }
 
-struct DeviceGuard {  // the caller's current device is put back on every path out
-  int prev = -1, dev;
-  bool ok;
-  explicit DeviceGuard(int d) : dev(d) {
-    if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
-    ok = prev == d || cudaSetDevice(d) == cudaSuccess;
-  }
-  ~DeviceGuard() {
-    if (prev >= 0 && prev != dev) cudaSetDevice(prev);
-  }
-};
-
 struct DeviceBuf {
   void* p = nullptr;
   cudaError_t alloc(size_t n) { return cudaMalloc(&p, n); }
