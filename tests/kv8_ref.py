@@ -69,10 +69,10 @@ def attention(q, k, v, pos0, scale, theta):
     group = nq // k.shape[1]
     q = rotate(q, pos0 + np.arange(n), theta)
     out = np.zeros_like(q)
-    for i in range(n):
-        for h in range(nq):
-            kk, vv = k[:pos0 + i + 1, h // group], v[:pos0 + i + 1, h // group]
-            x = kk @ q[i, h] * scale
-            p = np.exp(x - x.max())
-            out[i, h] = p @ vv / p.sum()
+    unseen = np.arange(k.shape[0])[None] > pos0 + np.arange(n)[:, None]
+    for h in range(nq):
+        x = q[:, h] @ k[:, h // group].T * scale
+        x[unseen] = -np.inf
+        p = np.exp(x - x.max(1, keepdims=True))
+        out[:, h] = p @ np.where(np.isnan(v[:, h // group]), 0, v[:, h // group]) / p.sum(1, keepdims=True)
     return out, q

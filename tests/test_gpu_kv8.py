@@ -349,3 +349,97 @@ def test_append_and_attention_in_a_captured_graph_on_another_stream():
                 r.ref.append(r.tables[b], at[b], kk[1][b:b + 1], vv[1][b:b + 1])
             r.check_out(out.double().cpu().numpy(), np.arange(4), at, [1] * 3, qq[1], 0.1)
         assert r.status() == (0, 0)
+
+
+@pytest.mark.parametrize("nq,nkv,d,lens,new", [
+    (1, 1, 128, [7990], [64]),             # one tile, its key steps cut over many CTAs
+    (2, 2, 64, [5000, 3], [70, 300]),      # and beside it tiles of another length
+    (1, 1, 128, [3], [333]),               # a group of one: the queries come in two passes
+    (5, 1, 128, [700], [128]),             # a group that does not divide 128
+    (32, 1, 64, [100, 2000], [9, 40]),
+    (64, 8, 64, [200], [1250]),            # enough tiles for 256 rows each
+    (16, 8, 128, [50], [4900]),
+    (48, 16, 64, [0, 9, 31], [600, 700, 500]),
+])
+def test_many_rows(nq, nkv, d, lens, new):
+    with Rig(len(lens), max(a + b for a, b in zip(lens, new)), nq=nq, nkv=nkv, d=d) as r:
+        r.append([0] * len(lens), [a + b for a, b in zip(lens, new)])
+        a = r.attend(lens, new, q=(q := r.rows(sum(new), nq)), pad=3)
+        b = r.attend(lens, new, q=q, pad=3, check=False)
+        assert torch.equal(a, b) and r.status() == (0, 0)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("scale", [-0.1, 1e-30])
+def test_odd_softmax_scales(new, scale):
+    with Rig(1, 200, nq=4, nkv=2) as r:
+        r.append([0], [150])
+        r.attend([150 - new], [new], scale=scale)
+
+
+@pytest.mark.parametrize("new", [12, 60])
+def test_rows_before_a_nan_do_not_see_it(new):
+    """The last page's first token is a NaN in K and V: only rows on that page may show it."""
+    n = 80
+    with Rig(1, 96, nq=2, nkv=2) as r:
+        r.append([0], [n])
+        k, v = r.rows(1), r.rows(1)
+        k[0][0, 1, 5] = v[0][0, 0, 9] = 0x7FC0
+        w = r.nkv * r.d
+        one, q = dev(np.array([n], np.int32)), r.rows(new, 2)
+        qtts.qtts_kv8_append(r.c, 0, 1, 1, 1, None, one, r.bt, r.stride, bits(k[0]), w, bits(v[0]), w)
+        out = torch.zeros(new, 2, 128, dtype=torch.bfloat16, device="cuda")
+        lens = n + 1 - new
+        qtts.qtts_kv8_attention(r.c, 0, 1, new, new, dev(np.array([0, new], np.int32)), dev(np.array([lens], np.int32)),
+                                r.bt, r.stride, bits(q[0]), 256, 0.1, out, 256, r.work)
+        got = out.double().cpu().numpy()
+        assert np.isnan(got[-1]).all() and np.isfinite(got[:-1]).all()
+        r.check_out(got[:-1], np.array([0, new - 1]), [lens], [new - 1], q[1][:-1], 0.1)
+
+
+def test_blocks_beyond_four_gigabytes():
+    """A layer's blocks start, and a page's lie, more than 2^32 bytes into the pool."""
+    pages, per = 140000, 8  # 8 kv heads x 4 KiB: 4.6 GB a layer
+    c = qtts.qtts_kv8_create(qtts.Kv8Config(2, 8, 8, 128, THETA, PAGE, 2, per * PAGE, pages))
+    try:
+        ids = np.concatenate((np.arange(pages - per, pages), np.arange(per))).astype(np.int32).reshape(2, per)
+        rng = np.random.default_rng(3)
+        k, v, q = (ref.bf16(rng.standard_normal((200, 8, 128))) for _ in range(3))
+        want = ref.Cache(16, 8, 128, THETA)
+        start, zero, bt = dev(np.array([0, 100, 200], np.int32)), dev(np.zeros(2, np.int32)), dev(ids)
+        work = torch.zeros(qtts.qtts_kv8_workspace_bytes(c), dtype=torch.uint8, device="cuda")
+        for layer in (1, 0):
+            qtts.qtts_kv8_append(c, layer, 2, 200, 100, start, zero, bt, per, bits(k[0]), 1024, bits(v[0]), 1024)
+        for b in range(2):
+            want.append(np.arange(8) + 8 * b, 0, k[1][100 * b:100 * b + 100], v[1][100 * b:100 * b + 100])
+        r = Rig.__new__(Rig)
+        r.B, r.nq, r.nkv, r.d, r.theta, r.ref, r.tables = 2, 8, 8, 128, THETA, want, np.arange(16).reshape(2, 8)
+        lens = dev(np.array([99, 99], np.int32))
+        for layer in (0, 1):
+            out = torch.zeros(2, 8, 128, dtype=torch.bfloat16, device="cuda")
+            qtts.qtts_kv8_attention(c, layer, 2, 2, 1, None, lens, bt, per, bits(q[0]), 1024, 0.1, out, 1024, work)
+            r.check_out(out.double().cpu().numpy(), np.arange(3), [99, 99], [1, 1], q[1][:2], 0.1)
+            out = torch.zeros(200, 8, 128, dtype=torch.bfloat16, device="cuda")
+            qtts.qtts_kv8_attention(c, layer, 2, 200, 100, start, zero, bt, per, bits(q[0]), 1024, 0.1, out, 1024, work)
+            r.check_out(out.double().cpu().numpy(), np.array([0, 100, 200]), [0, 0], [100, 100], q[1], 0.1)
+    finally:
+        qtts.qtts_kv8_destroy(c)
+
+
+def test_two_streams_with_a_workspace_each():
+    with Rig(2, 2100, nq=4, nkv=2) as r:
+        r.append([0, 0], [2100, 2100])
+        lens = [dev(np.array(x, np.int32)) for x in ([2099, 2000], [1500, 1999])]
+        qs = [r.rows(2, 4) for _ in range(2)]
+        works = [torch.zeros_like(r.work) for _ in range(2)]
+        outs = [torch.zeros(2, 4, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        dq = [bits(q[0]) for q in qs]
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for i, s in enumerate(streams):
+                qtts.qtts_kv8_attention(r.c, 0, 2, 2, 1, None, lens[i], r.bt, r.stride, dq[i], 512, 0.1, outs[i], 512,
+                                        works[i], s)
+        torch.cuda.synchronize()
+        for i, at in enumerate(([2099, 2000], [1500, 1999])):
+            r.check_out(outs[i].double().cpu().numpy(), np.arange(3), at, [1, 1], qs[i][1], 0.1)
