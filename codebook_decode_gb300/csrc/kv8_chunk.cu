@@ -154,6 +154,11 @@ template <int R>
 __device__ __forceinline__ void set_regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if one is
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -544,49 +549,71 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
         asm volatile("cp.async.wait_all;" ::: "memory");
         softmax_sync();
         const int quad = tid % kQuads * 4;
-#pragma unroll 2
-        for (int rl = tid / kQuads; rl < (count + kRowsOnce - 1) / kRowsOnce * kRowsOnce; rl += kRowsOnce) {
-          const int r = first + rl;
-          uint2 lo2 = make_uint2(0u, 0u), hi2 = lo2;
-          if (rl < count) {
-            lo2 = *(const uint2*)(raw + (rl * D + quad) * 2);
-            hi2 = *(const uint2*)(raw + (rl * D + D / 2 + quad) * 2);
+        constexpr int U = 4;  // rows at once: their reductions over lanes overlap
+#pragma unroll 1
+        for (int r1 = tid / kQuads; r1 < kRows && r1 - tid / kQuads < count; r1 += U * kRowsOnce) {
+          uint2 lo2[U], hi2[U];
+          uint32_t mag[U];
+#pragma unroll
+          for (int k = 0; k < U; ++k) {  // rows beyond the last are what stands there: nothing reads them
+            const uint8_t* src = raw + ((r1 + k * kRowsOnce) % kRows * D + quad) * 2;
+            lo2[k] = *(const uint2*)src;
+            hi2[k] = *(const uint2*)(src + D);
+            mag[k] = __vmaxu2(__vmaxu2(lo2[k].x & 0x7fff7fffu, lo2[k].y & 0x7fff7fffu),
+                              __vmaxu2(hi2[k].x & 0x7fff7fffu, hi2[k].y & 0x7fff7fffu));
+            mag[k] = max(mag[k] & 0xffffu, mag[k] >> 16);
           }
-          uint32_t mag = __vmaxu2(__vmaxu2(lo2.x & 0x7fff7fffu, lo2.y & 0x7fff7fffu), __vmaxu2(hi2.x & 0x7fff7fffu, hi2.y & 0x7fff7fffu));
-          mag = max(mag & 0xffffu, mag >> 16);
 #pragma unroll
-          for (int o = 1; o < kQuads; o <<= 1) mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, o));
-          const uint32_t ex = min(max(mag << 16 & 0x7f800000u, 1u << 23), 253u << 23);
-          const float inv = __uint_as_float((254u << 23) - ex) * a.q_sign;
-          const float lo[4] = {bf2f(lo2.x & 0xffffu), __uint_as_float(lo2.x & 0xffff0000u), bf2f(lo2.y & 0xffffu), __uint_as_float(lo2.y & 0xffff0000u)};
-          const float hi[4] = {bf2f(hi2.x & 0xffffu), __uint_as_float(hi2.x & 0xffff0000u), bf2f(hi2.y & 0xffffu), __uint_as_float(hi2.y & 0xffff0000u)};
-          float u[4], v[4];
-          const float* tr = (const float*)turn + (row_of(r) - tok) * D + quad;
+          for (int o = 1; o < kQuads; o <<= 1)
 #pragma unroll
-          for (int f = 0; f < 4; ++f) {
-            const float p = lo[f] * inv, q = hi[f] * inv;
-            u[f] = p;
-            v[f] = q;
-            if (a.c.rope_cos && rl < count) {
-              const float cs = tr[f], sn = tr[D / 2 + f];
-              u[f] = p * cs - q * sn;
-              v[f] = q * cs + p * sn;
+            for (int k = 0; k < U; ++k) mag[k] = max(mag[k], __shfl_xor_sync(0xffffffffu, mag[k], o));
+          float sum[U];  // of the rows' halves
+#pragma unroll
+          for (int k = 0; k < U; ++k) {
+            const int rl = r1 + k * kRowsOnce, r = first + rl;
+            const uint32_t ex = min(max(mag[k] << 16 & 0x7f800000u, 1u << 23), 253u << 23);
+            const float inv = __uint_as_float((254u << 23) - ex) * a.q_sign;
+            uint64_t p0 = pack2(__uint_as_float(lo2[k].x << 16) * inv, __uint_as_float(lo2[k].x & 0xffff0000u) * inv);
+            uint64_t p1 = pack2(__uint_as_float(lo2[k].y << 16) * inv, __uint_as_float(lo2[k].y & 0xffff0000u) * inv);
+            uint64_t q0 = pack2(__uint_as_float(hi2[k].x << 16) * inv, __uint_as_float(hi2[k].x & 0xffff0000u) * inv);
+            uint64_t q1 = pack2(__uint_as_float(hi2[k].y << 16) * inv, __uint_as_float(hi2[k].y & 0xffff0000u) * inv);
+            if (a.c.rope_cos) {
+              const uint8_t* tr = turn + min(row_of(r) - tok, tokens - 1) * (D * 4) + quad * 4;
+              const ulonglong2 cs = *(const ulonglong2*)tr;
+              const float4 s4 = *(const float4*)(tr + D * 2);
+              const uint64_t s0 = pack2(s4.x, s4.y), s1 = pack2(s4.z, s4.w), m0 = pack2(-s4.x, -s4.y), m1 = pack2(-s4.z, -s4.w);
+              const uint64_t u0 = p0, u1 = p1;
+              p0 = fma2(u0, cs.x, mul2(q0, m0));
+              p1 = fma2(u1, cs.y, mul2(q1, m1));
+              q0 = fma2(q0, cs.x, mul2(u0, s0));
+              q1 = fma2(q1, cs.y, mul2(u1, s1));
+            }
+            const uint64_t val[4] = {p0, p1, q0, q1};
+            uint32_t hu[4];
+            float part[4];
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+              const float2 y = unpack2(val[f]);
+              hu[f] = half2_bits(y.x, y.y);
+              const float2 z = __half22float2(*(const __half2*)&hu[f]);
+              part[f] = z.x + z.y;
+            }
+            sum[k] = (part[0] + part[1]) + (part[2] + part[3]);
+            if (rl < count) {
+              uint8_t* dst = sm.q[TWO ? r >> 7 : 0] + quad / 8 * kLboQ + (r & 127) / 8 * 128 + r % 8 * 16 + (quad & 4) * 2;
+              *(uint2*)dst = make_uint2(hu[0], hu[1]);
+              *(uint2*)(dst + D / 16 * kLboQ) = make_uint2(hu[2], hu[3]);
+              if (quad == 0) sm.ml[TWO ? r >> 7 : 1][r & 127].x = __uint_as_float(ex) * a.scale_log2;
             }
           }
-          const uint32_t hu[4] = {half2_bits(u[0], u[1]), half2_bits(u[2], u[3]), half2_bits(v[0], v[1]), half2_bits(v[2], v[3])};
-          float sum = 0.f;  // of the row's halves
 #pragma unroll
-          for (int f = 0; f < 4; ++f) {
-            const float2 y = __half22float2(*(const __half2*)&hu[f]);
-            sum += y.x + y.y;
-          }
+          for (int o = 1; o < kQuads; o <<= 1)
 #pragma unroll
-          for (int o = 1; o < kQuads; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          if (rl < count) {
-            uint8_t* dst = sm.q[TWO ? r >> 7 : 0] + quad / 8 * kLboQ + (r & 127) / 8 * 128 + r % 8 * 16 + (quad & 4) * 2;
-            *(uint2*)dst = make_uint2(hu[0], hu[1]);
-            *(uint2*)(dst + D / 16 * kLboQ) = make_uint2(hu[2], hu[3]);
-            if (quad == 0) sm.ml[TWO ? r >> 7 : 1][r & 127] = make_float2(__uint_as_float(ex) * a.scale_log2, 1152.f * sum);
+            for (int k = 0; k < U; ++k) sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], o);
+#pragma unroll
+          for (int k = 0; k < U; ++k) {
+            const int rl = r1 + k * kRowsOnce, r = first + rl;
+            if (quad == 0 && rl < count) sm.ml[TWO ? r >> 7 : 1][r & 127].y = 1152.f * sum[k];
           }
         }
         softmax_sync();  // before the next rows or the first weights take the place
@@ -608,12 +635,13 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
         const int step = w.p + i;
         const int lim = pos - step * kKeys;  // keys of the step that the row sees: those at <= lim
         const float4* sc = sm.sc[j & 3];
+        const bool masked = step >= first_masked;
         uint32_t r[2][32];  // half of the row's scores at a time
         auto load_scores = [&](int half) {
           tmem_ld32(r[0], ts + 64 * half);
           tmem_ld32(r[1], ts + 64 * half + 32);
           tmem_wait_ld();
-          if (step >= first_masked) {
+          if (masked) {
 #pragma unroll
             for (int n = 0; n < 64; ++n)
               if (64 * half + n / kPage * kPage + token_of(n % kPage) > lim) r[n / 32][n % 32] = 0xff800000u;  // -inf
@@ -623,8 +651,8 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
         // harmless ones, whatever its scales
         auto factors = [&](int page) {
           float4 f = sc[page];
-          if (page * kPage > lim) f = make_float4(1.f, 0.f, 1.f, 0.f);
-          f.x = fmaxf(f.x * cf, kKv8MinScale) + (f.x != f.x ? f.x : 0.f);  // positive: -inf stays -inf
+          if (masked && page * kPage > lim) f = make_float4(1.f, 0.f, 1.f, 0.f);
+          f.x = max_nan(f.x * cf, kKv8MinScale);  // positive: -inf stays -inf
           f.y = fmaf(-surplus, f.x, f.y);
           return f;
         };
@@ -756,18 +784,28 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
             tile[row * kHalf + ((y0 + e) ^ (row & (kHalf - 1)))] = make_float4(o[0][e], o[1][e], o[2][e], o[3][e]);
         }
         group_sync(x);
-#pragma unroll 2
-        for (int r1 = (warp & 3) * (32 / kHalf); r1 < min(kRows, cols - (TWO ? 128 * x : 0)); r1 += 4 * (32 / kHalf)) {
-          const int rl = r1 + lane / kHalf, y = lane % kHalf, r = TWO ? 128 * x + rl : rl;
-          if (r < cols) {
-            const float4 v = tile[rl * kHalf + (y ^ (rl & (kHalf - 1)))];
-            const float2 ml = sm.ml[x][rl];
+        constexpr int E = 4, kStep = 4 * (32 / kHalf);  // rows of a lane at once, rows of the group's warps
+        const int y = lane % kHalf, last = min(kRows, cols - (TWO ? 128 * x : 0));
+#pragma unroll 1
+        for (int r1 = (warp & 3) * (32 / kHalf) + lane / kHalf; r1 < last; r1 += E * kStep) {
+          float4 v[E];
+          float2 m2[E];
+#pragma unroll
+          for (int k = 0; k < E; ++k) {
+            const int rl = (r1 + k * kStep) % kRows;
+            v[k] = tile[rl * kHalf + (y ^ (rl & (kHalf - 1)))];
+            m2[k] = sm.ml[x][rl];
+          }
+#pragma unroll
+          for (int k = 0; k < E; ++k) {
+            const int rl = r1 + k * kStep, r = TWO ? 128 * x + rl : rl;
+            if (rl >= last) continue;
             if (starts && ends) {
-              write(r, half * kHalf + y, v, ml.y);
+              write(r, half * kHalf + y, v[k], m2[k].y);
             } else {
               float* part = a.part + ((size_t)(2 * blockIdx.x + starts) * kTile + r) * kCol;
-              *(float4*)(part + 4 * (half * kHalf + y)) = v;
-              if (y == 0) *(float2*)(part + D) = ml;
+              *(float4*)(part + 4 * (half * kHalf + y)) = v[k];
+              if (y == 0) *(float2*)(part + D) = m2[k];
             }
           }
         }
