@@ -5,7 +5,7 @@
 // of one session. For every 128 keys (8 pages)
 //   S [128 x 128] = Q . K^T,   O [128 x d] += P . V
 // with the accumulators in tensor memory and Q, K, V and P as half in shared
-// memory, in the canonical K-major layout without swizzle. Codes are exact in
+// memory, K-major with the 128-byte swizzle. Codes are exact in
 // half; the blocks' scales act outside the products, as in kv8_attention.cu:
 // the K scale on the scores, the V scale on the weights.
 //
@@ -42,14 +42,21 @@ constexpr int kChunkTries = 1 << 17;  // bound of each wait; a try sleeps up to 
 constexpr int kJoinSteps = 6;
 constexpr int kIssueWarp = (kSoftmaxThreads + kWidenThreads) / 32;
 
-// Bytes between the queries' core matrices along d: 16 more than their 128 rows
-// take, so that neighbouring lanes' stores fall on different banks (256 rows of
-// 128 dims leave no room for it).
-constexpr int lbo_q(int D, bool two) { return kRows * 16 + (D == 128 && two ? 0 : 16); }
+// Operands in shared memory: rows of 64 halves (128 bytes), rows one after the
+// other, 64-wide blocks of columns one after the other, and in a row the 16-byte
+// words exchanged by the row's low bits (the tensor cores' 128-byte swizzle), so
+// that neither a row's words nor a word of neighbouring rows share banks (the
+// unswizzled layout measured the same, with padding against bank conflicts).
+__device__ __forceinline__ int word_at(int row, int word) { return row * 128 + ((word ^ (row & 7)) << 4); }
+__device__ __forceinline__ uint64_t swizzled_desc(const void* p) {
+  return (uint64_t)((smem_addr(p) >> 4) & 0x3FFFu) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+// of the 16 columns (of k) number ks: their place in units of 16 bytes
+__host__ __device__ constexpr uint64_t k_step(int ks, int rows) { return (ks / 4 * rows * 128 + ks % 4 * 32) / 16; }
 
 template <int D, bool TWO>
 struct ChunkSmem {
-  alignas(128) uint8_t q[TWO ? 2 : 1][D / 8 * lbo_q(D, TWO)];
+  alignas(1024) uint8_t q[TWO ? 2 : 1][kRows * D * 2];
   uint8_t p[2][kRows * kKeys * 2];
   uint8_t k[2][kKeys * D * 2];
   uint8_t v[TWO ? 1 : 2][kKeys * D * 2];
@@ -328,7 +335,6 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
   };
   auto row_of = [&](int r) { return r * a.group_mul >> 16; };  // a tile row's query row
   // accumulators: S of group x at 128 x, O at 256 + 128 x
-  constexpr uint32_t kLboQ = lbo_q(D, TWO), kSbo = 128, kLboRow = kRows * 16, kLboV = D * 16;
 
   if (warp >= kSoftmaxThreads / 32 && warp < kIssueWarp) {
     set_regs_down<kRegsWiden>();
@@ -400,16 +406,16 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
           const float sv = v.y != v.y ? v.y : fmaxf(v.y, kKv8MinScale);
           sm.sc[j & 3][wp + lane] = make_float4(v.x, lg2(sv), 1.f / sv, 0.f);
         }
-        uint8_t* kd = sm.k[s] + 2 * dch * kLboRow + wp * 256 + r8 * 16;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int e = 0; e < kWords; ++e) {
             // as 1024 + byte: the score's surplus, 1152 times the query's sum, leaves in the softmax
             const uint4 k = wd[i][e];
-            uint8_t* dst = kd + i * 256 + 8 * (e % (D / 64)) * kLboRow + e / (D / 64) * 128;
-            *(uint4*)dst = make_uint4(raise_lo(k.x), raise_hi(k.x), raise_lo(k.y), raise_hi(k.y));
-            *(uint4*)(dst + kLboRow) = make_uint4(raise_lo(k.z), raise_hi(k.z), raise_lo(k.w), raise_hi(k.w));
+            uint8_t* dst = sm.k[s] + e % (D / 64) * (kKeys * 128);
+            const int row = (wp + i) * kPage + e / (D / 64) * 8 + r8;
+            *(uint4*)(dst + word_at(row, 2 * dch)) = make_uint4(raise_lo(k.x), raise_hi(k.x), raise_lo(k.y), raise_hi(k.y));
+            *(uint4*)(dst + word_at(row, 2 * dch + 1)) = make_uint4(raise_lo(k.z), raise_hi(k.z), raise_lo(k.w), raise_hi(k.w));
           }
       } else {
         const int vs = TWO ? 0 : s;
@@ -417,7 +423,6 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         // row r = (D / 4) jd + x4 of the V operand holds dim 4 x4 + jd
-        uint8_t* vd = sm.v[vs] + (wp * 2 + (D == 128 ? 0 : lane / D4)) * (D / 8) * 128 + x4 / 8 * 128 + x4 % 8 * 16;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -429,7 +434,8 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
               uint4 o;
               widen(w0[jd], o.x, o.y);
               widen(w1[jd], o.z, o.w);
-              *(uint4*)(vd + (2 * i + h) * (D / 8) * 128 + jd * (D4 / 8) * 128) = o;
+              const int key8 = 2 * (wp + i) + (D == 128 ? h : lane / D4);
+              *(uint4*)(sm.v[vs] + key8 / 8 * (D * 128) + word_at(jd * D4 + x4, key8 % 8)) = o;
             }
           }
       }
@@ -449,11 +455,10 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
         if (!(ok = wait(&sm.kfull[s], (jj >> 1) & 1))) return;
         tc_fence_after();
         // a descriptor's low bits are the address in 16-byte units: steps along k add to it
-        uint64_t qd = tc_smem_desc(smem_addr(sm.q[TWO ? x : 0]), kLboQ, kSbo);
-        uint64_t kd = tc_smem_desc(smem_addr(sm.k[s]), kLboRow, kSbo);
+        const uint64_t qd = swizzled_desc(sm.q[TWO ? x : 0]), kd = swizzled_desc(sm.k[s]);
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks, qd += 2 * kLboQ / 16, kd += 2 * kLboRow / 16)
-          tc_mma(tmem + 128 * x, qd, kd, idS, ks > 0);
+        for (int ks = 0; ks < D / 16; ++ks)
+          tc_mma(tmem + 128 * x, qd + k_step(ks, kRows), kd + k_step(ks, kKeys), idS, ks > 0);
         tc_commit(&sm.sdone[x]);
         mbar_arrive(&sm.sdone[x]);
         if (last) tc_commit(&sm.kdone[s]);
@@ -467,10 +472,10 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
         const int vs = TWO ? 0 : jj & 1;
         if (!(ok = wait(&sm.vfull[vs], TWO ? jj & 1 : (jj >> 1) & 1))) return;
         tc_fence_after();
-        uint64_t pd = tc_smem_desc(smem_addr(sm.p[x]), kLboRow, kSbo), vd = tc_smem_desc(smem_addr(sm.v[vs]), kLboV, kSbo);
+        const uint64_t pd = swizzled_desc(sm.p[x]), vd = swizzled_desc(sm.v[vs]);
 #pragma unroll
-        for (int ks = 0; ks < kKeys / 16; ++ks, pd += 2 * kLboRow / 16, vd += 2 * kLboV / 16)
-          tc_mma(tmem + 256 + 128 * x, pd, vd, idO, !first || ks > 0);
+        for (int ks = 0; ks < kKeys / 16; ++ks)
+          tc_mma(tmem + 256 + 128 * x, pd + k_step(ks, kRows), vd + k_step(ks, D), idO, !first || ks > 0);
         tc_commit(&sm.pvdone[x]);
         if (last) tc_commit(&sm.vdone[vs]);
       };
@@ -600,9 +605,10 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
             }
             sum[k] = (part[0] + part[1]) + (part[2] + part[3]);
             if (rl < count) {
-              uint8_t* dst = sm.q[TWO ? r >> 7 : 0] + quad / 8 * kLboQ + (r & 127) / 8 * 128 + r % 8 * 16 + (quad & 4) * 2;
-              *(uint2*)dst = make_uint2(hu[0], hu[1]);
-              *(uint2*)(dst + D / 16 * kLboQ) = make_uint2(hu[2], hu[3]);
+              // dims quad.. and D / 2 + quad..
+              uint8_t* dst = sm.q[TWO ? r >> 7 : 0] + (quad & 4) * 2;
+              *(uint2*)(dst + word_at(r & 127, quad / 8)) = make_uint2(hu[0], hu[1]);
+              *(uint2*)(dst + (D == 128 ? kRows * 128 + word_at(r & 127, quad / 8) : word_at(r & 127, 4 + quad / 8))) = make_uint2(hu[2], hu[3]);
               if (quad == 0) sm.ml[TWO ? r >> 7 : 1][r & 127].x = __uint_as_float(ex) * a.scale_log2;
             }
           }
@@ -694,9 +700,8 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
             tmem_wait_st();
           }
         }
-        uint8_t* dst = sm.p[x] + row / 8 * 128 + row % 8 * 16;
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half, dst += 8 * kLboRow) {
+        for (int half = 0; half < 2; ++half) {
           load_scores(half);
 #pragma unroll
           for (int page = 0; page < kPagesPerStep / 2; ++page) {
@@ -714,8 +719,9 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
             }
             const float2 t = unpack2(sum);
             l = fmaf(t.x + t.y, f.z, l);
-            *(uint4*)(dst + 2 * page * kLboRow) = make_uint4(h[0], h[1], h[2], h[3]);
-            *(uint4*)(dst + (2 * page + 1) * kLboRow) = make_uint4(h[4], h[5], h[6], h[7]);
+            uint8_t* dst = sm.p[x] + half * (kRows * 128);
+            *(uint4*)(dst + word_at(row, 2 * page)) = make_uint4(h[0], h[1], h[2], h[3]);
+            *(uint4*)(dst + word_at(row, 2 * page + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
           }
         }
         fence_async_shared();
