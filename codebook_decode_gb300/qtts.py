@@ -145,9 +145,10 @@ def ptr(a):
     """Data pointer of a torch tensor / numpy array / None."""
     if a is None:
         return None
-    if hasattr(a, "data_ptr"):
+    try:
         return a.data_ptr()
-    return a.ctypes.data
+    except AttributeError:
+        return a.ctypes.data
 
 
 def _check(model, rc):
@@ -158,8 +159,8 @@ def _check(model, rc):
 
 
 def _stream(s):
-    if s is None:
-        return None
+    if s is None or type(s) is int:
+        return s
     return s.cuda_stream if hasattr(s, "cuda_stream") else s
 
 
