@@ -343,6 +343,12 @@ int fail(qtts_kv8* c, int code, const char* fmt, ...) {
   return code;
 }
 
+// A failed launch is reported here, not by the caller's next CUDA call.
+int launch_fault(qtts_kv8* c, const char* who, cudaError_t e) {
+  cudaGetLastError();
+  return fail(c, QTTS_E_CUDA, "%s: %s", who, cudaGetErrorString(e));
+}
+
 const char* config_fault(const qtts_kv8_config& c) {
   if (c.n_layers <= 0 || c.n_q_heads <= 0 || c.n_kv_heads <= 0 || c.pool_pages <= 0) return "sizes must be positive";
   if (c.head_dim != 64 && c.head_dim != 128) return "head_dim must be 64 or 128";
@@ -354,6 +360,8 @@ const char* config_fault(const qtts_kv8_config& c) {
   if (c.max_context <= 0 || c.max_context > kKv8MaxContext) return "max_context must be in 1..262144";
   if (!(c.rope_theta >= 0.f) || std::isinf(c.rope_theta)) return "rope_theta must be finite and not negative";
   if ((long long)c.pool_pages * c.n_kv_heads > 0x7fffffffll) return "pool_pages x n_kv_heads must be below 2^31";
+  // bytes of the codes stay countable (an allocation of 2^52 fails, one of 2^64 would be taken for 0)
+  if ((long long)c.pool_pages * c.n_kv_heads > (1ll << 40) / c.n_layers) return "n_layers x pool_pages x n_kv_heads must be at most 2^40";
   return nullptr;
 }
 
@@ -439,7 +447,7 @@ int qtts_kv8_create(const qtts_kv8_config* cfg, int device, qtts_kv8** out) {
   if (e == cudaSuccess && cfg->rope_theta > 0.f) e = cudaMalloc((void**)&c->rope_cos, table);
   if (e == cudaSuccess && cfg->rope_theta > 0.f) e = cudaMalloc((void**)&c->rope_sin, table);
   if (e != cudaSuccess) {
-    cudaGetLastError();  // the failed allocation's sticky-free error is reported here, not by a later call
+    cudaGetLastError();  // reported here, not by a later call
     return bail(QTTS_E_OOM, "device allocation", e);
   }
   // pages start as zero scales: a page that was never appended to reads as 0
@@ -520,7 +528,7 @@ int qtts_kv8_append(qtts_kv8* c, int layer, int B, int n_rows, int max_new, cons
   const dim3 grid(B * touched, (2 * f.n_kv_heads + warps - 1) / warps);
   const cudaError_t e = launch(f.head_dim == 64 ? append_kernel<64> : append_kernel<128>, grid, warps * 32,
                                (cudaStream_t)stream, view(c, layer), q, touched, k, k_stride, v, v_stride);
-  if (e != cudaSuccess) return fail(c, QTTS_E_CUDA, "qtts_kv8_append: %s", cudaGetErrorString(e));
+  if (e != cudaSuccess) return launch_fault(c, "qtts_kv8_append", e);
   return QTTS_OK;
 }
 
@@ -544,7 +552,7 @@ int qtts_kv8_read(qtts_kv8* c, int layer, int B, int n_rows, int max_new, const 
   const dim3 grid(B * touched, (2 * f.n_kv_heads + warps - 1) / warps);
   const cudaError_t e = launch(f.head_dim == 64 ? read_kernel<64> : read_kernel<128>, grid, warps * 32,
                                (cudaStream_t)stream, view(c, layer), q, touched, k_out, v_out);
-  if (e != cudaSuccess) return fail(c, QTTS_E_CUDA, "qtts_kv8_read: %s", cudaGetErrorString(e));
+  if (e != cudaSuccess) return launch_fault(c, "qtts_kv8_read", e);
   return QTTS_OK;
 }
 
@@ -571,7 +579,7 @@ int qtts_kv8_attention(qtts_kv8* c, int layer, int B, int n_rows, int max_new, c
   if (!g.ok) return fail(c, QTTS_E_CUDA, "cudaSetDevice failed");
   const cudaError_t e = kv8_attention(view(c, layer), qb, f.head_dim, f.n_q_heads / f.n_kv_heads, c->G, q, q_stride,
                                       scale, out, out_stride, workspace, (cudaStream_t)stream);
-  if (e != cudaSuccess) return fail(c, QTTS_E_CUDA, "qtts_kv8_attention: %s", cudaGetErrorString(e));
+  if (e != cudaSuccess) return launch_fault(c, "qtts_kv8_attention", e);
   return QTTS_OK;
 }
 

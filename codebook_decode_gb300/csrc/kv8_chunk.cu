@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
     // Shares, and the place where this CTA's begins. Whole tiles where the most
     // that a CTA gets is not worse than an equal share and the cost of joining
     // cut tiles (reading queries twice, partials out and in: kJoinSteps).
-    int total = 0, tiles = 0, most = 0, per = 0, own = 0, lo = 0, share = 0;
+    int total = 0, tiles = 0, most = 0, per = 0, own = 0, lo = 0, share = 0, rows = 0;
     bool whole = false;
     long long u0 = 0, u1 = 0;
     Kv8Session ses;
@@ -272,6 +272,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
         carry += __shfl_sync(0xffffffffu, x, 31);
         if (!pass) {
           tiles += __reduce_add_sync(0xffffffffu, count * a.c.nkv);
+          rows += __reduce_add_sync(0xffffffffu, ses.n);
           most = max(most, __reduce_max_sync(0xffffffffu, ses.n ? (ses.L + ses.n + kKeys - 1) / kKeys : 0));
         } else if (lo <= u0 && u0 < (long long)lo + own) {
           const int at = (int)(u0 - lo), h = at / per;
@@ -283,6 +284,11 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
         }
       }
       if (pass == 0) {
+        // sessions that share rows (a row_start that goes back): the work would not be bounded by n_rows
+        if (rows > a.q.n_rows) {
+          set_err(a.c.err, QTTS_DEV_BAD_SESSION);
+          break;
+        }
         total = carry;
         const int G = gridDim.x;
         share = max((total + G - 1) / G, 4);
@@ -897,7 +903,7 @@ size_t kv8_chunk_workspace(int d, int sms) { return 2 * (size_t)sms * 2 * kRows 
 
 bool kv8_chunk_fits(const Kv8View& v, const Kv8Batch& q, int group, long long pages) {
   const long long tiles = q.n_rows / (kRows / group) + q.B, steps = pages * kPage / kKeys + 2;
-  return tiles * v.nkv < (1ll << 31) / steps;
+  return tiles * v.nkv < ((1ll << 31) - 4096) / steps;  // 4096: rounding up to shares
 }
 
 cudaError_t kv8_chunk(const Kv8View& v, const Kv8Batch& q, int d, int group, int sms, const uint16_t* qp,

@@ -554,7 +554,10 @@ int qtts_w4_linear(qtts_w4* w, int M, const uint16_t* x, int64_t x_stride, void*
   while ((1 << a.s_log) < kW4MaxSplit && ctas << a.s_log < w->G && w->KT >= (4 * kw) << a.s_log) ++a.s_log;
   if (M <= 8) e = w4_launch<1, 1>(a, s);
   else e = M <= 16 ? w4_launch<2, 2>(a, s) : M <= 32 ? w4_launch<4, 2>(a, s) : w4_launch<8, 2>(a, s);
-  if (e != cudaSuccess) return fail(w, QTTS_E_CUDA, "qtts_w4_linear: %s", cudaGetErrorString(e));
+  if (e != cudaSuccess) {
+    cudaGetLastError();  // reported here, not by the caller's next CUDA call
+    return fail(w, QTTS_E_CUDA, "qtts_w4_linear: %s", cudaGetErrorString(e));
+  }
   return QTTS_OK;
 }
 

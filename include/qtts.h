@@ -401,7 +401,9 @@ int qtts_frame_weight_bytes(const qtts_model* m, int64_t* bytes);
  * scale and the new values' one; where it grows, the codes already there
  * become round-half-even(code * (old scale / new scale)). Scales, reciprocals,
  * ratios and these products are binary32. A row that lands on
- * slot 0 of a page starts its blocks anew, so freed pages need no clearing.
+ * slot 0 of a page starts its blocks anew, so freed pages need no clearing; a
+ * session may also go back to an earlier length and append there (the scale of
+ * the block it lands in keeps counting what was taken back).
  *
  * Calls take a batch of B sessions with their rows packed: session b has the
  * rows row_start[b] .. row_start[b + 1] - 1 (device [B + 1]; NULL: exactly one
@@ -417,11 +419,17 @@ int qtts_frame_weight_bytes(const qtts_model* m, int64_t* bytes);
  * may be slices of one projection's output. Calls are asynchronous on
  * `stream`, allocate nothing and can be captured into a graph; the caller's
  * current device is left as it was.
+ * The lengths and tables that a call reads must not change while it runs.
+ * Kernels start early where the one before them on the stream allows it, and
+ * wait for that one before they touch what is passed to them: stream order
+ * holds.
  * Device-side checks: a session whose rows do not fit row_start, max_new,
  * max_context or its block table is skipped (QTTS_DEV_BAD_SESSION); a page id
  * outside the pool is not written, and what attention gives for that session
- * is unspecified (QTTS_DEV_BAD_PAGE). Other sessions go on. The first error is
- * kept until qtts_kv8_status reads it.
+ * is unspecified (QTTS_DEV_BAD_PAGE). Other sessions go on; a row_start that
+ * goes back leaves the rows' results unspecified. The first error is
+ * kept until qtts_kv8_status reads it. After QTTS_DEV_TIMEOUT the results of
+ * that call are unspecified and its workspace has to be zeroed again.
  * ------------------------------------------------------------------------- */
 typedef struct qtts_kv8 qtts_kv8;
 
@@ -459,7 +467,8 @@ int qtts_kv8_append(qtts_kv8* c, int layer, int B, int n_rows, int max_new, cons
  *   out = sum_j softmax_j(scale * q_rot . K_j) V_j
  * q: rows of [n_q_heads][head_dim], not yet rotated (they are rotated like K
  * here, in fp32); out: the same shape. Query head h reads kv head
- * h / (n_q_heads / n_kv_heads). workspace: qtts_kv8_workspace_bytes of device
+ * h / (n_q_heads / n_kv_heads). out must not overlap q. workspace:
+ * qtts_kv8_workspace_bytes (41 MB at head_dim 128, 21 at 64) of device
  * memory, 16-byte aligned, zeroed once before its first call and left ready
  * for the next one; calls that may overlap (on several streams, or captured
  * into graphs that may run at once) need one each. Results do not depend on
@@ -477,8 +486,9 @@ int qtts_kv8_read(qtts_kv8* c, int layer, int B, int n_rows, int max_new, const 
                   const int32_t* pos0, const int32_t* block_tables, int bt_stride, uint16_t* k_out, uint16_t* v_out,
                   void* stream);
 
-/* Wait for the device, then read and clear the cache's error word
- * (QTTS_DEV_*). Returns QTTS_E_DEVICE / QTTS_E_TIMEOUT when it was set. */
+/* Wait for the device (so not while a stream is being captured), then read and
+ * clear the cache's error word (QTTS_DEV_*). Returns QTTS_E_DEVICE /
+ * QTTS_E_TIMEOUT when it was set. */
 int qtts_kv8_status(qtts_kv8* c, int* device_err);
 
 /* ---------------------------------------------------------------------------

@@ -70,6 +70,12 @@ int main() {
     const int rc = qtts_kv8_create(&f, 0, &out);
     printf("config_%d %d %s\n", i, out ? -99 : rc, qtts_kv8_last_error(nullptr));
   }
+  {
+    qtts_kv8_config f = {1 << 26, 1, 1, 128, 1e6f, 16, 4, 4096, 1 << 26};
+    qtts_kv8* out = &c;
+    const int rc = qtts_kv8_create(&f, 0, &out);
+    printf("config_bytes %d %s\n", out ? -99 : rc, qtts_kv8_last_error(nullptr));
+  }
   say("free_not_allocated", (c.page_used.assign(100, 0), c.seen_now.assign(100, 0), [&] {
         const int32_t id = 3;
         return qtts_kv8_free_pages(&c, 1, &id);

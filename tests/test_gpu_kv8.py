@@ -443,3 +443,43 @@ def test_two_streams_with_a_workspace_each():
         torch.cuda.synchronize()
         for i, at in enumerate(([2099, 2000], [1500, 1999])):
             r.check_out(outs[i].double().cpu().numpy(), np.arange(3), at, [1, 1], qs[i][1], 0.1)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_attention_over_a_page_outside_the_pool_reports_it(new):
+    with Rig(3, 128) as r:
+        r.append([0] * 3, [100] * 3)
+        bt = r.tables.copy()
+        bt[1, 2] = -1
+        bt[1, 4] = 2 ** 31 - 1
+        q, lens = r.rows(3 * new, 4), [100 - new] * 3
+        out = torch.zeros(3 * new, 4, 128, dtype=torch.bfloat16, device="cuda")
+        start = np.arange(4) * new
+        qtts.qtts_kv8_attention(r.c, 0, 3, 3 * new, new, dev(start.astype(np.int32)), dev(np.array(lens, np.int32)),
+                                dev(bt), r.stride, bits(q[0]), 512, 0.1, out, 512, r.work)
+        assert r.status() == (qtts.QTTS_E_DEVICE, qtts.QTTS_DEV_BAD_PAGE)
+        r.check_out(out.double().cpu().numpy(), start, [lens[0], -1, lens[2]], [new] * 3, q[1], 0.1)
+        r.attend(lens, [new] * 3)
+        assert r.status() == (0, 0)
+
+
+def test_the_largest_batch():
+    with Rig(1024, 20, nq=2, nkv=1, d=64) as r:
+        lens = [int(x) for x in r.rng.integers(0, 19, 1024)]
+        r.append([0] * 1024, [x + 1 for x in lens])
+        r.attend(lens, [1] * 1024, one=True)
+        r.append([-1] * 1023 + [lens[-1] + 1], [0] * 1023 + [1])
+        assert r.status() == (0, 0)
+
+
+def test_sessions_that_share_rows_are_reported():
+    with Rig(3, 128) as r:
+        r.append([0] * 3, [100] * 3)
+        q, lens = r.rows(40, 4), dev(np.array([60] * 3, np.int32))
+        out = torch.zeros(40, 4, 128, dtype=torch.bfloat16, device="cuda")
+        start = dev(np.array([0, 40, 0, 40], np.int32))
+        qtts.qtts_kv8_attention(r.c, 0, 3, 40, 40, start, lens, dev(r.tables), r.stride, bits(q[0]), 512, 0.1, out, 512,
+                                r.work)
+        assert r.status() == (qtts.QTTS_E_DEVICE, qtts.QTTS_DEV_BAD_SESSION)
+        r.attend([60] * 3, [40] * 3)
+        assert r.status() == (0, 0)

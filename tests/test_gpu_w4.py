@@ -55,7 +55,7 @@ def check(y, x, q, s, group, f32):
 
 
 @pytest.mark.parametrize("group", [32, 64, 128])
-@pytest.mark.parametrize("N,K", [(1, 1), (16, 1), (17, 3), (40, 5), (129, 7), (1000, 9), (2048, 16), (333, 48)])
+@pytest.mark.parametrize("N,K", [(1, 1), (16, 1), (17, 3), (40, 5), (129, 7), (1000, 9), (2048, 16), (333, 49)])
 @pytest.mark.parametrize("M", [1, 3, 8, 9, 16, 17, 32, 33, 64])
 def test_products(M, N, K, group):
     K *= group
@@ -138,3 +138,42 @@ def test_refusals():
         assert code(1, x[:, 4:], 136, y, 64, f32) == qtts.QTTS_E_INVALID
         assert code(1, x, 136, y, 63, f32) == qtts.QTTS_E_INVALID
         assert qtts.qtts_w4_linear(L.w, 0, None, 136, None, 64, f32) == 0
+
+
+@pytest.mark.parametrize("M,N,K,group", [(64, 40, 20000, 32), (33, 5000, 8192, 128), (8, 20, 60000 // 64 * 64, 64)])
+def test_more_activations_than_shared_memory_holds(M, N, K, group):
+    rng = np.random.default_rng(K)
+    q = rng.integers(-8, 8, (N, K)).astype(np.int8)
+    sb, s = bf16(np.exp(rng.standard_normal((N, K // group))))
+    xb, x = bf16(rng.standard_normal((M, K)))
+    with Linear(N, K, group) as L:
+        qtts.qtts_w4_load(L.w, q, sb)
+        y = torch.zeros(M, N, device="cuda")
+        qtts.qtts_w4_linear(L.w, M, bits(xb), K, y, N, qtts.QTTS_DTYPE_F32)
+        check(y.double().cpu().numpy(), x, q, s, group, True)
+
+
+def test_back_to_back_products_wait_for_their_input():
+    """Products that start early read their activations only when the one before has written them."""
+    rng = np.random.default_rng(9)
+    N = 512
+    wb, w = bf16(rng.standard_normal((N, N)) * N ** -0.5)
+    q, sb, s = quantize(w, 64)
+    xb, x = bf16(rng.standard_normal((4, N)))
+    with Linear(N, N, 64) as L:
+        qtts.qtts_w4_quantize(L.w, bits(wb))
+        a, b = bits(xb), torch.zeros(4, N, dtype=torch.bfloat16, device="cuda")
+        c = torch.zeros_like(b)
+        for _ in range(50):
+            b.fill_(float("nan"))
+            qtts.qtts_w4_linear(L.w, 4, a, N, b, N, qtts.QTTS_DTYPE_BF16)
+            qtts.qtts_w4_linear(L.w, 4, b, N, c, N, qtts.QTTS_DTYPE_BF16)
+            qtts.qtts_w4_linear(L.w, 4, c, N, b, N, qtts.QTTS_DTYPE_BF16)
+        check(c.double().cpu().numpy(), bf16_twice(L, a, N), q, s, 64, False)
+
+
+def bf16_twice(L, a, N):
+    y = torch.zeros(4, N, dtype=torch.bfloat16, device="cuda")
+    qtts.qtts_w4_linear(L.w, 4, a, N, y, N, qtts.QTTS_DTYPE_BF16)
+    torch.cuda.synchronize()
+    return y.double().cpu().numpy()

@@ -31,7 +31,7 @@ def code(said, name):
     "append_one_each_max", "append_null_len", "append_null_table", "append_null_k", "append_null_v", "append_k_align",
     "append_k_narrow", "append_v_odd", "attend_null_q", "attend_null_out", "attend_q_narrow", "attend_out_align",
     "attend_null_work", "attend_work_align", "attend_scale_nan", "attend_scale_inf", "attend_too_much", "read_null_k",
-    "read_v_align"] + ["config_%d" % i for i in range(10)])
+    "read_v_align", "config_bytes"] + ["config_%d" % i for i in range(10)])
 def test_bad_arguments_are_refused_with_a_message(said, name):
     assert code(said, name) == qtts.QTTS_E_INVALID
     assert len(said[name].split(" ", 1)[1]) > 8
