@@ -4,18 +4,27 @@
 // A tile is up to 128 or 256 rows (query tokens x the q heads of one kv head)
 // of one session. For every 128 keys (8 pages)
 //   S [128 x 128] = Q . K^T,   O [128 x d] += P . V
-// with the accumulators in tensor memory and Q, K, V and P as half in shared
-// memory, K-major with the 128-byte swizzle. Codes are exact in
-// half; the blocks' scales act outside the products, as in kv8_attention.cu:
-// the K scale on the scores, the V scale on the weights.
+// with S, P and O in tensor memory (P takes the place of the scores it comes
+// from) and Q, K and V as half in shared memory, K-major with the 128-byte
+// swizzle. Codes are exact in half; the blocks' scales act outside the
+// products, as in kv8_attention.cu: the K scale on the scores, the V scale on
+// the weights.
 //
-// Warps: two softmax groups of four (a thread per row), four warps that widen
-// the codes of the step after into shared memory, and one thread that issues
+// Warps: two softmax groups of four (a thread per row), four warps that widen a
+// step's K codes into shared memory, four for its V codes, and one that issues
 // the products. With 256 rows the groups have 128 each and a step's widened
 // codes serve both; with 128 they take the steps in turn, each with its own S,
 // P, O, maximum and sum, which are joined at the tile's end. Either way one
-// group's softmax runs beside the other's products. Bound by the instructions
-// of softmax and widening, which run next to the products.
+// group's softmax runs beside the other's products.
+//
+// Bound by the chain of a group's step (scores, maximum, weights, product: some
+// 5500 cycles for two steps, against 2200 of their four products) and by what
+// comes before and after: 1024 rows behind 1000 tokens, 16 q and 8 kv heads of
+// 128, take 32 us (0.39 PFLOP/s), of which 6 us go before the first step and 3
+// after the last; 30000 tokens back 332 us (0.77 PFLOP/s).
+// What moved it most was code size and local memory: with the waits unrolled and
+// each role's place in the work in registers the code had 165 KB, did not stay in
+// the instruction cache, and spilled into a first-level cache of a few KB (40 us).
 //
 // Work is cut into equal shares of key steps, one per CTA; tiles that several
 // CTAs share are joined through the workspace by the last to arrive, in order.
@@ -24,6 +33,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "kv8.cuh"
 #include "kv8_attn.cuh"
@@ -35,40 +45,30 @@ constexpr int kRows = 128, kKeys = 128, kPagesPerStep = kKeys / kPage;
 constexpr int kSoftmaxThreads = 256, kWidenThreads = 256;
 constexpr int kThreadsC = kSoftmaxThreads + kWidenThreads + 128;
 // registers of a thread: launched, then of the softmax, widening and issuing groups
-constexpr int kRegsLaunch = 96, kRegsSoftmax = 144, kRegsWiden = 64, kRegsIssue = 64;
+constexpr int kRegsLaunch = 96, kRegsSoftmax = 144, kRegsWiden = 72, kRegsIssue = 48;
 static_assert(kSoftmaxThreads * kRegsSoftmax + kWidenThreads * kRegsWiden + 128 * kRegsIssue <= kThreadsC * kRegsLaunch,
               "the groups share what the block was launched with");
 constexpr int kChunkTries = 1 << 17;  // bound of each wait; a try sleeps up to about 10 us
+// What a cut tile costs beside its steps (queries prepared twice, partials out and in),
+// in key steps: 6 and 12 measured the same, 3 and 0 cut calls that take 32 us whole into
+// 44 us.
 constexpr int kJoinSteps = 6;
+// Pairs of pages unrolled in the passes for the maximum and for the weights, where no
+// row is masked: 2 and 4 measured 32.4 us, 1 and 2 34.0, 4 and 4 33.0.
+constexpr int kTurnsMax = 2, kTurnsWeights = 4;
 constexpr int kIssueWarp = (kSoftmaxThreads + kWidenThreads) / 32;
+constexpr int kPlaces = kWidenThreads / 32 + 2, kIssuePlace = kPlaces - 2, kSoftmaxPlace = kPlaces - 1;
 
 // Operands in shared memory: rows of 64 halves (128 bytes), rows one after the
 // other, 64-wide blocks of columns one after the other, and in a row the 16-byte
 // words exchanged by the row's low bits (the tensor cores' 128-byte swizzle), so
-// that neither a row's words nor a word of neighbouring rows share banks (the
-// unswizzled layout measured the same, with padding against bank conflicts).
+// that neither a row's words nor a word of neighbouring rows share banks.
 __device__ __forceinline__ int word_at(int row, int word) { return row * 128 + ((word ^ (row & 7)) << 4); }
 __device__ __forceinline__ uint64_t swizzled_desc(const void* p) {
   return (uint64_t)((smem_addr(p) >> 4) & 0x3FFFu) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 // of the 16 columns (of k) number ks: their place in units of 16 bytes
 __host__ __device__ constexpr uint64_t k_step(int ks, int rows) { return (ks / 4 * rows * 128 + ks % 4 * 32) / 16; }
-
-template <int D, bool TWO>
-struct ChunkSmem {
-  alignas(1024) uint8_t q[TWO ? 2 : 1][kRows * D * 2];
-  uint8_t p[2][kRows * kKeys * 2];
-  uint8_t k[2][kKeys * D * 2];
-  uint8_t v[TWO ? 1 : 2][kKeys * D * 2];
-  float2 ml[2][kRows];  // each group's maximum and sum; before the first step the rows' query scales and offsets
-  float4 sc[4][kPagesPerStep];  // a page's K scale, logarithm and reciprocal of its V scale
-  // kfull, vfull: widened; kdone, vdone: read by the products; sdone: a group's
-  // scores are there; pfull: its weights; pvdone: its second product has run;
-  // qfull: the tile's queries; drained: after a failure, all products issued
-  uint64_t kfull[2], vfull[2], kdone[2], vdone[2], sdone[2], pfull[2], pvdone[2], qfull, drained;
-  uint32_t tmem;
-  int failed, verdict, flag, share, whole, start_b, start_h, start_t, start_p, total;
-};
 
 struct ChunkArgs {
   Kv8View c;
@@ -79,7 +79,7 @@ struct ChunkArgs {
   float scale_log2, q_sign;  // |softmax scale| log2 e, and its sign
   uint16_t* out;
   int64_t out_stride;
-  float* part;        // [2 CTAs][tile rows][D + 4]
+  float* part;        // [2 CTAs][D / 4][tile rows] float4, then [tile rows] maximum and sum (D + 4 floats a row)
   unsigned* arrived;  // [CTAs]
 };
 
@@ -87,11 +87,14 @@ __device__ __forceinline__ int tile_steps(int L, int n, int t, int rows_per_tile
   return (L + min((t + 1) * rows_per_tile, n) + kKeys - 1) / kKeys;
 }
 
-// A place in the work: key step p of tile t of kv head h of session b.
+// A place in the work: key step p of tile t of kv head h of session b. Each role
+// keeps its own in shared memory: in registers it pushed others out to local
+// memory, which misses the little first-level cache that is left.
 struct Place {
   int b, h, t, p, steps;
   Kv8Session s;
   __device__ __forceinline__ void enter(const ChunkArgs& a, int bb) {
+#pragma unroll 1
     for (b = bb; b < a.q.B; ++b) {
       s = kv8_session(a.q, b, a.c.max_context, a.c.err);
       if (s.n) break;
@@ -114,12 +117,30 @@ struct Place {
   }
   __device__ __forceinline__ void advance(const ChunkArgs& a, int n) {
     p += n;
+#pragma unroll 1
     while (p >= steps) {
       const int over = p - steps;
       next_tile(a);
       p = over;
     }
   }
+};
+
+template <int D, bool TWO>
+struct ChunkSmem {
+  alignas(1024) uint8_t q[TWO ? 2 : 1][kRows * D * 2];
+  uint8_t out[kRows * D * 2 * (TWO ? 2 : 1)];  // results on their way out
+  uint8_t k[2][kKeys * D * 2];
+  uint8_t v[TWO ? 1 : 2][kKeys * D * 2];
+  float2 ml[2][kRows];  // each group's maximum and sum; before the first step the rows' query scales
+  float4 sc[4][kPagesPerStep];  // a page's K scale, logarithm and reciprocal of its V scale
+  // kfull, vfull: widened; kdone, vdone: read by the products; sdone: a group's
+  // scores are there; pfull: its weights; pvdone: its second product has run;
+  // qfull: the tile's queries; drained: after a failure, all products issued
+  uint64_t kfull[2], vfull[2], kdone[2], vdone[2], sdone[2], pfull[2], pvdone[2], qfull, drained;
+  Place at[kPlaces];  // of the widening warps, the issuing warp and the softmax groups
+  uint32_t tmem;
+  int failed, verdict, flag, share, units;
 };
 
 // A session's tiles, weighed by their key steps (or 1 each: whole), up to the
@@ -139,9 +160,16 @@ __device__ __forceinline__ int tiles_until(const Kv8Session& s, int rows_per_til
   return t;
 }
 
-template <int N>
-__device__ __forceinline__ void copy_async(void* dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_addr(dst)), "l"(src), "n"(N) : "memory");
+// Loads into their registers or not: a choice after the load would wait for it.
+__device__ __forceinline__ void load_if(uint4& v, const void* p, bool yes) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n @p ld.global.v4.u32 {%0,%1,%2,%3}, [%4];\n}"
+               : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+               : "l"(p), "r"((uint32_t)yes));
+}
+__device__ __forceinline__ void load_if(float2& v, const void* p, bool yes) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %3, 0;\n @p ld.global.v2.f32 {%0,%1}, [%2];\n}"
+               : "+f"(v.x), "+f"(v.y)
+               : "l"(p), "r"((uint32_t)yes));
 }
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
@@ -150,9 +178,6 @@ __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy
 __device__ __forceinline__ void softmax_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
 }
-__device__ __forceinline__ void group_sync(int x) {  // one softmax group
-  asm volatile("bar.sync %0, %1;" ::"r"(2 + x), "n"(kSoftmaxThreads / 2) : "memory");
-}
 template <int R>
 __device__ __forceinline__ void set_regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
@@ -160,6 +185,10 @@ __device__ __forceinline__ void set_regs_up() {
 template <int R>
 __device__ __forceinline__ void set_regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+__device__ __forceinline__ uint32_t bf2_bits(float a, float b) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+  return *(const uint32_t*)&p;
 }
 __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if one is
   float d;
@@ -171,18 +200,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
 constexpr uint32_t idesc_f16(int M, int N) {  // kind::f16: fp32 accumulator, half A and B, both K-major
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-__device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t at) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(at));
 }
 __device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t at) {
   asm volatile(
@@ -191,6 +215,11 @@ __device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t at) {
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(at));
 }
+__device__ __forceinline__ void tmem_st8(uint32_t at, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
@@ -198,17 +227,26 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) 
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld8(uint32_t (&r)[8], uint32_t at) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+__device__ __forceinline__ void tmem_ld4(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(at));
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// the same, for the registers of a load that was asked for earlier: their use stays behind it
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+// A from tensor memory: a row's halves two to a column
+__device__ __forceinline__ void tc_mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// codes 0, 1 and 2, 3 of four as 1024 + byte
-__device__ __forceinline__ uint32_t raise_lo(uint32_t c) { return __byte_perm(c, 0x64646464u, 0x4140); }
-__device__ __forceinline__ uint32_t raise_hi(uint32_t c) { return __byte_perm(c, 0x64646464u, 0x4342); }
 
 // The order in which a page's 16 tokens stand along the key axis of both
 // products: that of the V blocks' words. Place n holds token_of(n).
@@ -277,10 +315,13 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
         } else if (lo <= u0 && u0 < (long long)lo + own) {
           const int at = (int)(u0 - lo), h = at / per;
           int sum;
-          sm.start_b = b0 + lane;
-          sm.start_h = h;
-          sm.start_t = tiles_until(ses, a.rows_per_tile, whole, at - h * per, sum);
-          sm.start_p = at - h * per - sum;
+          Place& w = sm.at[0];
+          w.b = b0 + lane;
+          w.h = h;
+          w.t = tiles_until(ses, a.rows_per_tile, whole, at - h * per, sum);
+          w.p = at - h * per - sum;
+          w.steps = tile_steps(ses.L, ses.n, w.t, a.rows_per_tile);
+          w.s = ses;
         }
       }
       if (pass == 0) {
@@ -298,45 +339,38 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
         if (u0 >= u1) break;
       }
     }
+    // key steps of this CTA
+    __syncwarp();
+    const Place first = sm.at[0];
+    int units = (int)max(u1 - u0, 0ll);
+    if (whole && units) {
+      Place x = first;
+      const int count = units;
+      units = x.steps;
+#pragma unroll 1
+      for (int i = 1; i < count; ++i) {
+        x.next_tile(a);
+        units += x.steps;
+      }
+    }
+    if (lane > 0 && lane < kPlaces) sm.at[lane] = first;
     if (lane == 0) {
       sm.share = share;
-      sm.whole = whole;
-      sm.total = (int)max(u1 - u0, 0ll);
+      sm.units = units;
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
-  const int share = sm.share;
-  const long long u0 = (long long)blockIdx.x * share;  // of a cut
-  int units = sm.total;  // key steps of this CTA
-  Place w;
-  if (units) {
-    w.enter(a, sm.start_b);
-    w.h = sm.start_h;
-    w.t = sm.start_t;
-    w.p = sm.start_p;
-    w.steps = tile_steps(w.s.L, w.s.n, w.t, a.rows_per_tile);
-    if (sm.whole) {
-      Place x = w;
-      const int tiles = units;
-      units = 0;
-      for (int i = 0; i < tiles; ++i) {
-        units += x.steps;
-        if (i + 1 < tiles) x.next_tile(a);
-      }
-    }
-  }
-  // bounded; once one wait has run out all others give up too
+  const int units = sm.units;
+  // Bounded; once one wait has run out all others give up too. Short: it is in many places.
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (mbar_test(bar, parity)) return true;
-    for (int tries = 0; tries < kChunkTries; ++tries) {
+#pragma unroll 1
+    for (int tries = 0; tries < kChunkTries && !*(volatile int*)&sm.failed; ++tries)
       if (mbar_test_sleep(bar, parity, 10000)) return true;
-      if (*(volatile int*)&sm.failed) return false;
-    }
-    sm.failed = 1;
-    set_err(a.c.err, QTTS_DEV_TIMEOUT);
+    *(volatile int*)&sm.failed = 1;
     return false;
   };
   auto row_of = [&](int r) { return r * a.group_mul >> 16; };  // a tile row's query row
@@ -349,11 +383,11 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
     // a warp takes 2 of a step's pages
     const bool is_v = warp >= kSoftmaxThreads / 32 + 4;
     const int wp = (warp & 3) * 2;
-    int j = 0;
+    int j;
     bool ok = true;
     // lane x holds the block of page x & 1 of this warp's two, of step 16 k + x / 2
     // (-1: beyond the tile); the next 16 steps' are fetched meanwhile
-    Place ahead = w;
+    Place& ahead = sm.at[warp - kSoftmaxThreads / 32];
     auto fetch_ids = [&](int k) {
       int id = -1;
       if (16 * k + (lane >> 1) < units) {
@@ -369,10 +403,17 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
           id = page * a.c.nkv + x.h;
         }
       }
-      if (16 * (k + 1) < units) ahead.advance(a, 16);
+      __syncwarp();
+      if (lane == 0 && 16 * (k + 1) < units) {
+        Place x = ahead;
+        x.advance(a, 16);
+        ahead = x;
+      }
+      __syncwarp();
       return id;
     };
-    int left = units, ids = -1, ids_next = -1;
+    int ids = -1, ids_next = -1;
+    const int left = units;
     // K: a lane of a load is one of 8 tokens x 4 words. V: lane x takes the 4 dims
     // 4x.. (d = 64: of half the words)
     constexpr int D4 = D / 4, kWords = D / 32;  // 16-byte words of a lane and page
@@ -381,142 +422,170 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
     uint4 wd[2][kWords];
     float2 sc[2];
     auto load = [&](int step) {
-      const int from = (step ^ j) & 16 ? ids_next : ids;
       const uint4 none = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);  // codes of 0
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int id = __shfl_sync(0xffffffffu, from, 2 * (step & 15) + i);
+        const int id = __shfl_sync(0xffffffffu, ids, 2 * (step & 15) + i);
         const uint8_t* src = a.c.codes + (size_t)max(id, 0) * (32 * D) + lane_at;
 #pragma unroll
         for (int e = 0; e < kWords; ++e) {
           const int at = is_v ? e * 16 : e % (D / 64) * 1024 + token_of(e / (D / 64) * 8 + r8) * 64;
-          wd[i][e] = id >= 0 ? *(const uint4*)(src + at) : none;
+          wd[i][e] = none;
+          load_if(wd[i][e], src + at, id >= 0);
         }
-        sc[i] = !is_v && id >= 0 ? *(const float2*)(a.c.scales + 2 * (size_t)id) : make_float2(0.f, 0.f);
+        sc[i] = make_float2(0.f, 0.f);
+        load_if(sc[i], a.c.scales + 2 * (size_t)max(id, 0), !is_v && id >= 0);
       }
     };
-    if (left) {
-      ids = fetch_ids(0);
-      load(0);
-    }
-    for (; left; ++j, --left) {
-      if ((j & 15) == 0 && j) ids = ids_next;
-      if ((j & 15) == 8) ids_next = fetch_ids((j >> 4) + 1);
-      const int s = j & 1;
-      if (!is_v) {
-        if (j >= 2) ok = wait(&sm.kdone[s], ((j >> 1) - 1) & 1);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        if (lane < 2) {
-          const float2 v = lane ? sc[1] : sc[0];
-          const float sv = v.y != v.y ? v.y : fmaxf(v.y, kKv8MinScale);
-          sm.sc[j & 3][wp + lane] = make_float4(v.x, lg2(sv), 1.f / sv, 0.f);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int e = 0; e < kWords; ++e) {
-            // as 1024 + byte: the score's surplus, 1152 times the query's sum, leaves in the softmax
-            const uint4 k = wd[i][e];
-            uint8_t* dst = sm.k[s] + e % (D / 64) * (kKeys * 128);
-            const int row = (wp + i) * kPage + e / (D / 64) * 8 + r8;
-            *(uint4*)(dst + word_at(row, 2 * dch)) = make_uint4(raise_lo(k.x), raise_hi(k.x), raise_lo(k.y), raise_hi(k.y));
-            *(uint4*)(dst + word_at(row, 2 * dch + 1)) = make_uint4(raise_lo(k.z), raise_hi(k.z), raise_lo(k.w), raise_hi(k.w));
+    // step -1 only asks for the first step's codes
+#pragma unroll 1
+    for (j = -1; j < left; ++j) {
+      if (j >= 0) {
+        const int s = j & 1;
+        if (!is_v) {
+          if (j >= 2) ok = wait(&sm.kdone[s], ((j >> 1) - 1) & 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane < 2) {
+            const float2 v = lane ? sc[1] : sc[0];
+            const float sv = v.y != v.y ? v.y : fmaxf(v.y, kKv8MinScale);
+            sm.sc[j & 3][wp + lane] = make_float4(v.x, lg2(sv), 1.f / sv, 0.f);
           }
-      } else {
-        const int vs = TWO ? 0 : s;
-        if (j >= (TWO ? 1 : 2)) ok = wait(&sm.vdone[vs], TWO ? (j - 1) & 1 : ((j >> 1) - 1) & 1);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        // row r = (D / 4) jd + x4 of the V operand holds dim 4 x4 + jd
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int h = 0; h < kWords / 2; ++h) {
-            const uint4 v0 = wd[i][2 * h], v1 = wd[i][2 * h + 1];
-            const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
-#pragma unroll
-            for (int jd = 0; jd < 4; ++jd) {
-              uint4 o;
-              widen(w0[jd], o.x, o.y);
-              widen(w1[jd], o.z, o.w);
-              const int key8 = 2 * (wp + i) + (D == 128 ? h : lane / D4);
-              *(uint4*)(sm.v[vs] + key8 / 8 * (D * 128) + word_at(jd * D4 + x4, key8 % 8)) = o;
+            for (int e = 0; e < kWords; ++e) {
+              const uint4 k = wd[i][e];
+              uint8_t* dst = sm.k[s] + e % (D / 64) * (kKeys * 128);
+              const int row = (wp + i) * kPage + e / (D / 64) * 8 + r8;
+              uint4 lo, hi;
+              widen(k.x, lo.x, lo.y);
+              widen(k.y, lo.z, lo.w);
+              widen(k.z, hi.x, hi.y);
+              widen(k.w, hi.z, hi.w);
+              *(uint4*)(dst + word_at(row, 2 * dch)) = lo;
+              *(uint4*)(dst + word_at(row, 2 * dch + 1)) = hi;
             }
-          }
+        } else {
+          const int vs = TWO ? 0 : s;
+          if (j >= (TWO ? 1 : 2)) ok = wait(&sm.vdone[vs], TWO ? (j - 1) & 1 : ((j >> 1) - 1) & 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          // row r = (D / 4) jd + x4 of the V operand holds dim 4 x4 + jd
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int h = 0; h < kWords / 2; ++h) {
+              const uint4 v0 = wd[i][2 * h], v1 = wd[i][2 * h + 1];
+              const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+              for (int jd = 0; jd < 4; ++jd) {
+                uint4 o;
+                widen(w0[jd], o.x, o.y);
+                widen(w1[jd], o.z, o.w);
+                const int key8 = 2 * (wp + i) + (D == 128 ? h : lane / D4);
+                *(uint4*)(sm.v[vs] + key8 / 8 * (D * 128) + word_at(jd * D4 + x4, key8 % 8)) = o;
+              }
+            }
+        }
+        fence_async_shared();
+        mbar_arrive(is_v ? &sm.vfull[TWO ? 0 : s] : &sm.kfull[s]);
       }
-      fence_async_shared();
-      mbar_arrive(is_v ? &sm.vfull[TWO ? 0 : s] : &sm.kfull[s]);
-      if (left > 1) load(j + 1);
+      if (j < 0 || (j & 15) == 8) {
+        ids_next = fetch_ids((j + 8) >> 4);
+        if (j < 0) ids = ids_next;
+      }
+      if ((j & 15) == 15 && j > 0) ids = ids_next;
+      if (j + 1 < left) load(j + 1);
     }
   } else if (warp >= kIssueWarp) {
     // ---- products
     set_regs_down<kRegsIssue>();
-    if (warp == kIssueWarp && lane == 0) {
+    if (warp == kIssueWarp) {
+      // The whole warp goes through the loop, so that descriptors stay in uniform
+      // registers; one lane, always the same, issues.
+      const bool leader = elect_one();
       constexpr uint32_t idS = idesc_f16(kRows, kKeys), idO = idesc_f16(kRows, D);
-      int j = 0, seg = 0, left = units, n[2] = {0, 0};  // n: steps of each group
+      int j = 0, seg = 0, left = units;
+      uint32_t odd = 0;  // bit x: group x has had an odd number of steps
       bool ok = true;
       auto scores = [&](int jj, int x, bool last) {  // group x's scores of step jj; last: K's place is free after
         const int s = jj & 1;
-        if (!(ok = wait(&sm.kfull[s], (jj >> 1) & 1))) return;
+        ok = __all_sync(0xffffffffu, wait(&sm.kfull[s], (jj >> 1) & 1));
+        if (!ok) return;
         tc_fence_after();
         // a descriptor's low bits are the address in 16-byte units: steps along k add to it
         const uint64_t qd = swizzled_desc(sm.q[TWO ? x : 0]), kd = swizzled_desc(sm.k[s]);
+        if (leader) {
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          tc_mma(tmem + 128 * x, qd + k_step(ks, kRows), kd + k_step(ks, kKeys), idS, ks > 0);
-        tc_commit(&sm.sdone[x]);
-        mbar_arrive(&sm.sdone[x]);
-        if (last) tc_commit(&sm.kdone[s]);
+          for (int ks = 0; ks < D / 16; ++ks)
+            tc_mma(tmem + 128 * x, qd + k_step(ks, kRows), kd + k_step(ks, kKeys), idS, ks > 0);
+          tc_commit(&sm.sdone[x]);
+          mbar_arrive(&sm.sdone[x]);
+          if (last) tc_commit(&sm.kdone[s]);
+        }
+        __syncwarp();
       };
       auto weights_there = [&](int x) {  // group x has read its scores and written its weights
-        ok = wait(&sm.pfull[x], n[x] & 1);
-        ++n[x];
+        ok = __all_sync(0xffffffffu, wait(&sm.pfull[x], odd >> x & 1));
+        odd ^= 1u << x;
         return ok;
       };
       auto values = [&](int jj, int x, bool first, bool last) {  // group x's second product of step jj
         const int vs = TWO ? 0 : jj & 1;
-        if (!(ok = wait(&sm.vfull[vs], TWO ? jj & 1 : (jj >> 1) & 1))) return;
+        ok = __all_sync(0xffffffffu, wait(&sm.vfull[vs], TWO ? jj & 1 : (jj >> 1) & 1));
+        if (!ok) return;
         tc_fence_after();
-        const uint64_t pd = swizzled_desc(sm.p[x]), vd = swizzled_desc(sm.v[vs]);
+        const uint64_t vd = swizzled_desc(sm.v[vs]);
+        if (leader) {
 #pragma unroll
-        for (int ks = 0; ks < kKeys / 16; ++ks)
-          tc_mma(tmem + 256 + 128 * x, pd + k_step(ks, kRows), vd + k_step(ks, D), idO, !first || ks > 0);
-        tc_commit(&sm.pvdone[x]);
-        if (last) tc_commit(&sm.vdone[vs]);
+          for (int ks = 0; ks < kKeys / 16; ++ks)
+            tc_mma_tmem(tmem + 256 + 128 * x, tmem + 128 * x + 8 * ks, vd + k_step(ks, D), idO, !first || ks > 0);
+          tc_commit(&sm.pvdone[x]);
+          if (last) tc_commit(&sm.vdone[vs]);
+        }
+        __syncwarp();
       };
+      // A group's next scores land where its weights stood: the product that reads
+      // those has to have run (products on different accumulators may pass each other).
+      auto weights_read = [&](int x) { return ok = __all_sync(0xffffffffu, wait(&sm.pvdone[x], (odd >> x & 1) ^ 1)); };
+#pragma unroll 1
       while (left && ok) {
+        const Place& w = sm.at[kIssuePlace];
         const int cnt = min(left, w.steps - w.p), j0 = j, j1 = j + cnt;
-        ok = wait(&sm.qfull, seg & 1);
+        ok = __all_sync(0xffffffffu, wait(&sm.qfull, seg & 1));
         tc_fence_after();
         if constexpr (TWO) {
           const bool both = min(a.rows_per_tile, w.s.n - w.t * a.rows_per_tile) * a.group > kRows;
 #pragma unroll 1
           for (int x = 0; x <= both && ok; ++x) scores(j, x, x == both);
+#pragma unroll 1
           for (; j < j1 && ok; ++j)
 #pragma unroll 1
             for (int x = 0; x <= both && ok; ++x) {
-              // the group's next scores first: it waits for them, not for the values
-              if (weights_there(x) && j + 1 < j1) scores(j + 1, x, x == both);
-              if (ok) values(j, x, j == j0, x == both);
+              if (weights_there(x)) values(j, x, j == j0, x == both);
+              if (ok && j + 1 < j1 && weights_read(x)) scores(j + 1, x, x == both);
             }
         } else {
 #pragma unroll 1
           for (int i = 0; i < min(cnt, 2) && ok; ++i) scores(j + i, (j + i) & 1, true);
+#pragma unroll 1
           for (; j < j1 && ok; ++j) {
-            if (weights_there(j & 1) && j + 2 < j1) scores(j + 2, j & 1, true);
-            if (ok) values(j, j & 1, j - j0 < 2, true);
+            if (weights_there(j & 1)) values(j, j & 1, j - j0 < 2, true);
+            if (ok && j + 2 < j1 && weights_read(j & 1)) scores(j + 2, j & 1, true);
           }
         }
         left -= cnt;
         ++seg;
-        w.p += cnt;
-        if (w.p == w.steps) w.next_tile(a);
+        __syncwarp();
+        if (leader && left) sm.at[kIssuePlace].advance(a, cnt);
+        __syncwarp();
       }
       if (!ok) {  // what was issued has to end before the tensor memory is given back
-        tc_commit(&sm.drained);
+        if (leader) tc_commit(&sm.drained);
+#pragma unroll 1
         for (int tries = 0; tries < kChunkTries; ++tries)
-          if (mbar_test(&sm.drained, 0)) break;
+          if (mbar_test_sleep(&sm.drained, 0, 10000)) break;
       }
     }
     __syncwarp();
@@ -526,217 +595,197 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
     const int x = warp >> 2, row = tid & 127;
     const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + 128 * x + quarter, to = tmem + 256 + quarter;
-    int j = 0, left = units, n = 0;  // n: steps of this group
+    int j = 0, left = units;
+    uint32_t odd = 0;  // this group has had an odd number of steps
     bool ok = true;
+    const Place& w = sm.at[kSoftmaxPlace];
+#pragma unroll 1
     while (left && ok) {
       const int cnt = min(left, w.steps - w.p);
       const int row0 = w.t * a.rows_per_tile, rows = min(a.rows_per_tile, w.s.n - row0), cols = rows * a.group;
-      const int pos = w.s.L + row0 + min(row_of(TWO ? tid : row), rows - 1);  // last position that this row sees
       const bool active = !TWO || x == 0 || cols > kRows;
-      // The tile's queries, rotated, into shared memory. They and their rotations
-      // are copied to the weights' place first, up to 128 rows at a time, all
-      // copies in flight at once (loaded into registers they took a memory
-      // latency for every few rows). A thread then takes 4 dims of a row and
-      // their partners D/2 further, D/8 lanes a row. Scaled by the power of two
-      // of the row's largest magnitude (before the rotation, which can grow it by
-      // sqrt 2: half has room).
-      constexpr int kQuads = D / 8, kRowsOnce = kSoftmaxThreads / kQuads;
-      uint8_t* raw = sm.p[0];                    // [128][D] bf16
-      uint8_t* turn = sm.p[0] + kRows * D * 2;   // [tokens][D / 2 cosines, D / 2 sines]; tokens x D x 4 <= 128 x D x 2
-      const int pass_tokens = a.group > 1 ? kRows * a.group_mul >> 16 : kRows / 2;
+      // The tile's queries, rotated, into shared memory: four lanes a row, each with
+      // every fourth 4 dims and their partners D/2 further. Scaled by the power of
+      // two of the row's largest magnitude (before the rotation, which can grow it
+      // by sqrt 2: half has room).
+      constexpr int kQuads = D / 32;  // of a lane
 #pragma unroll 1
-      for (int tok = 0; tok < rows; tok += pass_tokens) {
-        const int tokens = min(pass_tokens, rows - tok), first = tok * a.group, count = tokens * a.group;
-        for (int i = tid; i < count * (D / 4); i += kSoftmaxThreads) {
-          const int r = first + i / (D / 4), at = i % (D / 4) * 4, rq = row_of(r);
-          copy_async<8>(raw + i * 8, a.qp + (int64_t)(w.s.r0 + row0 + rq) * a.q_stride + (size_t)(w.h * a.group + r - rq * a.group) * D + at);
-        }
-        if (a.c.rope_cos)
-          for (int i = tid; i < tokens * (D / 4); i += kSoftmaxThreads) {
-            const int at = i % (D / 8) * 4;
-            const float* src = i / (D / 8) & 1 ? a.c.rope_sin : a.c.rope_cos;
-            copy_async<16>(turn + i * 16, src + (size_t)(w.s.L + row0 + tok + i / (D / 4)) * (D / 2) + at);
-          }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        softmax_sync();
-        const int quad = tid % kQuads * 4;
-        constexpr int U = 4;  // rows at once: their reductions over lanes overlap
-#pragma unroll 1
-        for (int r1 = tid / kQuads; r1 < kRows && r1 - tid / kQuads < count; r1 += U * kRowsOnce) {
-          uint2 lo2[U], hi2[U];
-          uint32_t mag[U];
+      for (int r = tid / 4; r - tid / 4 < cols; r += kSoftmaxThreads / 4) {
+        const int rc = min(r, cols - 1), rq = row_of(rc), at = tid % 4 * 4;
+        const uint16_t* src = a.qp + (int64_t)(w.s.r0 + row0 + rq) * a.q_stride + (size_t)(w.h * a.group + rc - rq * a.group) * D + at;
+        const size_t turn = (size_t)(w.s.L + row0 + rq) * (D / 2) + at;
+        uint2 lo[kQuads], hi[kQuads];
+        ulonglong2 cs[kQuads];
+        float4 sn[kQuads];
 #pragma unroll
-          for (int k = 0; k < U; ++k) {  // rows beyond the last are what stands there: nothing reads them
-            const uint8_t* src = raw + ((r1 + k * kRowsOnce) % kRows * D + quad) * 2;
-            lo2[k] = *(const uint2*)src;
-            hi2[k] = *(const uint2*)(src + D);
-            mag[k] = __vmaxu2(__vmaxu2(lo2[k].x & 0x7fff7fffu, lo2[k].y & 0x7fff7fffu),
-                              __vmaxu2(hi2[k].x & 0x7fff7fffu, hi2[k].y & 0x7fff7fffu));
-            mag[k] = max(mag[k] & 0xffffu, mag[k] >> 16);
-          }
-#pragma unroll
-          for (int o = 1; o < kQuads; o <<= 1)
-#pragma unroll
-            for (int k = 0; k < U; ++k) mag[k] = max(mag[k], __shfl_xor_sync(0xffffffffu, mag[k], o));
-          float sum[U];  // of the rows' halves
-#pragma unroll
-          for (int k = 0; k < U; ++k) {
-            const int rl = r1 + k * kRowsOnce, r = first + rl;
-            const uint32_t ex = min(max(mag[k] << 16 & 0x7f800000u, 1u << 23), 253u << 23);
-            const float inv = __uint_as_float((254u << 23) - ex) * a.q_sign;
-            uint64_t p0 = pack2(__uint_as_float(lo2[k].x << 16) * inv, __uint_as_float(lo2[k].x & 0xffff0000u) * inv);
-            uint64_t p1 = pack2(__uint_as_float(lo2[k].y << 16) * inv, __uint_as_float(lo2[k].y & 0xffff0000u) * inv);
-            uint64_t q0 = pack2(__uint_as_float(hi2[k].x << 16) * inv, __uint_as_float(hi2[k].x & 0xffff0000u) * inv);
-            uint64_t q1 = pack2(__uint_as_float(hi2[k].y << 16) * inv, __uint_as_float(hi2[k].y & 0xffff0000u) * inv);
-            if (a.c.rope_cos) {
-              const uint8_t* tr = turn + min(row_of(r) - tok, tokens - 1) * (D * 4) + quad * 4;
-              const ulonglong2 cs = *(const ulonglong2*)tr;
-              const float4 s4 = *(const float4*)(tr + D * 2);
-              const uint64_t s0 = pack2(s4.x, s4.y), s1 = pack2(s4.z, s4.w), m0 = pack2(-s4.x, -s4.y), m1 = pack2(-s4.z, -s4.w);
-              const uint64_t u0 = p0, u1 = p1;
-              p0 = fma2(u0, cs.x, mul2(q0, m0));
-              p1 = fma2(u1, cs.y, mul2(q1, m1));
-              q0 = fma2(q0, cs.x, mul2(u0, s0));
-              q1 = fma2(q1, cs.y, mul2(u1, s1));
-            }
-            const uint64_t val[4] = {p0, p1, q0, q1};
-            uint32_t hu[4];
-            float part[4];
-#pragma unroll
-            for (int f = 0; f < 4; ++f) {
-              const float2 y = unpack2(val[f]);
-              hu[f] = half2_bits(y.x, y.y);
-              const float2 z = __half22float2(*(const __half2*)&hu[f]);
-              part[f] = z.x + z.y;
-            }
-            sum[k] = (part[0] + part[1]) + (part[2] + part[3]);
-            if (rl < count) {
-              // dims quad.. and D / 2 + quad..
-              uint8_t* dst = sm.q[TWO ? r >> 7 : 0] + (quad & 4) * 2;
-              *(uint2*)(dst + word_at(r & 127, quad / 8)) = make_uint2(hu[0], hu[1]);
-              *(uint2*)(dst + (D == 128 ? kRows * 128 + word_at(r & 127, quad / 8) : word_at(r & 127, 4 + quad / 8))) = make_uint2(hu[2], hu[3]);
-              if (quad == 0) sm.ml[TWO ? r >> 7 : 1][r & 127].x = __uint_as_float(ex) * a.scale_log2;
-            }
-          }
-#pragma unroll
-          for (int o = 1; o < kQuads; o <<= 1)
-#pragma unroll
-            for (int k = 0; k < U; ++k) sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], o);
-#pragma unroll
-          for (int k = 0; k < U; ++k) {
-            const int rl = r1 + k * kRowsOnce, r = first + rl;
-            if (quad == 0 && rl < count) sm.ml[TWO ? r >> 7 : 1][r & 127].y = 1152.f * sum[k];
+        for (int k = 0; k < kQuads; ++k) {
+          lo[k] = *(const uint2*)(src + 16 * k);
+          hi[k] = *(const uint2*)(src + 16 * k + D / 2);
+          if (a.c.rope_cos) {
+            cs[k] = *(const ulonglong2*)(a.c.rope_cos + turn + 16 * k);
+            sn[k] = *(const float4*)(a.c.rope_sin + turn + 16 * k);
           }
         }
-        softmax_sync();  // before the next rows or the first weights take the place
+        uint32_t mag = 0;
+#pragma unroll
+        for (int k = 0; k < kQuads; ++k)
+          mag = __vmaxu2(mag, __vmaxu2(__vmaxu2(lo[k].x & 0x7fff7fffu, lo[k].y & 0x7fff7fffu),
+                                       __vmaxu2(hi[k].x & 0x7fff7fffu, hi[k].y & 0x7fff7fffu)));
+        mag = __vmaxu2(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
+        mag = __vmaxu2(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
+        mag = max(mag & 0xffffu, mag >> 16);
+        const uint32_t ex = min(max(mag << 16 & 0x7f800000u, 1u << 23), 253u << 23);
+        const float inv = __uint_as_float((254u << 23) - ex) * a.q_sign;
+        if (r < cols && at == 0) sm.ml[TWO ? r >> 7 : 1][r & 127].x = __uint_as_float(ex) * a.scale_log2;
+        uint8_t* dst = sm.q[TWO ? r >> 7 : 0] + (at & 4) * 2;
+#pragma unroll
+        for (int k = 0; k < kQuads; ++k) {
+          uint64_t p0 = pack2(__uint_as_float(lo[k].x << 16) * inv, __uint_as_float(lo[k].x & 0xffff0000u) * inv);
+          uint64_t p1 = pack2(__uint_as_float(lo[k].y << 16) * inv, __uint_as_float(lo[k].y & 0xffff0000u) * inv);
+          uint64_t q0 = pack2(__uint_as_float(hi[k].x << 16) * inv, __uint_as_float(hi[k].x & 0xffff0000u) * inv);
+          uint64_t q1 = pack2(__uint_as_float(hi[k].y << 16) * inv, __uint_as_float(hi[k].y & 0xffff0000u) * inv);
+          if (a.c.rope_cos) {
+            const uint64_t s0 = pack2(sn[k].x, sn[k].y), s1 = pack2(sn[k].z, sn[k].w);
+            const uint64_t m0 = pack2(-sn[k].x, -sn[k].y), m1 = pack2(-sn[k].z, -sn[k].w);
+            const uint64_t u0 = p0, u1 = p1;
+            p0 = fma2(u0, cs[k].x, mul2(q0, m0));
+            p1 = fma2(u1, cs[k].y, mul2(q1, m1));
+            q0 = fma2(q0, cs[k].x, mul2(u0, s0));
+            q1 = fma2(q1, cs[k].y, mul2(u1, s1));
+          }
+          const float2 y0 = unpack2(p0), y1 = unpack2(p1), z0 = unpack2(q0), z1 = unpack2(q1);
+          if (r < cols) {  // dims 16 k + at.. and D / 2 + 16 k + at..
+            const int word = 2 * k + at / 8;
+            *(uint2*)(dst + word_at(r & 127, word)) = make_uint2(half2_bits(y0.x, y0.y), half2_bits(y1.x, y1.y));
+            *(uint2*)(dst + (D == 128 ? kRows * 128 + word_at(r & 127, word) : word_at(r & 127, 4 + word))) =
+                make_uint2(half2_bits(z0.x, z0.y), half2_bits(z1.x, z1.y));
+          }
+        }
       }
-      const float cf = sm.ml[TWO ? x : 1][row].x, surplus = sm.ml[TWO ? x : 1][row].y;
+      softmax_sync();
+      const float cf = sm.ml[TWO ? x : 1][row].x;
       fence_async_shared();
       tc_fence_before();  // the last tile's accumulators have been read
       mbar_arrive(&sm.qfull);
 
       float m = kNone, l = 0.f;
-      int mine = 0;  // steps of this group in this tile
-      const int first_masked = (w.s.L + row0 + 1) / kKeys;
-      for (int i = 0; i < cnt && ok; ++i, ++j) {
+      bool any = false;  // steps of this group in this tile
+      // of the tile's keys from this CTA's first step on: the last that this row
+      // sees, and the step from which on a row does not see all
+      int lim = w.s.L + row0 + min(row_of(TWO ? 128 * x + row : row), rows - 1) - w.p * kKeys;
+      const int first_masked = j + (w.s.L + row0 + 1) / kKeys - w.p;
+#pragma unroll 1
+      for (const int end = j + cnt; j < end && ok; ++j, lim -= kKeys) {
         if (TWO ? !active : (j & 1) != x) continue;
-        ok = wait(&sm.sdone[x], n & 1);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = __all_sync(0xffffffffu, wait(&sm.sdone[x], odd));
         if (!ok) break;
         tc_fence_after();
-        const int step = w.p + i;
-        const int lim = pos - step * kKeys;  // keys of the step that the row sees: those at <= lim
         const float4* sc = sm.sc[j & 3];
-        const bool masked = step >= first_masked;
-        uint32_t r[2][32];  // half of the row's scores at a time
-        auto load_scores = [&](int half) {
-          tmem_ld32(r[0], ts + 64 * half);
-          tmem_ld32(r[1], ts + 64 * half + 32);
-          tmem_wait_ld();
-          if (masked) {
+        // One path for steps that every row sees whole and one for the others: the
+        // first without jumps (each costs an instruction fetch).
+        auto work = [&](auto masked) {
+          constexpr bool kMasked = decltype(masked)::value;
+          // The scores come a page at a time, the next page's load beside the work on
+          // this one: first from the last page down, for the maximum, then up again.
+          // Two pages a turn: unrolled in full, the roles' code outgrew the instruction
+          // cache.
+          uint32_t r0[16], r1[16];
+          auto load = [&](uint32_t (&v)[16], int page) { tmem_ld16(v, ts + 16 * page); };
+          auto mask = [&](uint32_t (&v)[16], int page) {
+            if constexpr (kMasked) {
 #pragma unroll
-            for (int n = 0; n < 64; ++n)
-              if (64 * half + n / kPage * kPage + token_of(n % kPage) > lim) r[n / 32][n % 32] = 0xff800000u;  // -inf
-          }
-        };
-        // a page's factors: of one that the row does not see at all they are
-        // harmless ones, whatever its scales
-        auto factors = [&](int page) {
-          float4 f = sc[page];
-          if (masked && page * kPage > lim) f = make_float4(1.f, 0.f, 1.f, 0.f);
-          f.x = max_nan(f.x * cf, kKv8MinScale);  // positive: -inf stays -inf
-          f.y = fmaf(-surplus, f.x, f.y);
-          return f;
-        };
-        float mx = kNone;
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          load_scores(half);
-#pragma unroll
-          for (int page = 0; page < kPagesPerStep / 2; ++page) {
-            auto at = [&](int e) { return __uint_as_float(r[page / 2][page % 2 * 16 + e]); };
+              for (int n = 0; n < 16; ++n)
+                if (page * kPage + token_of(n) > lim) v[n] = 0xff800000u;  // -inf
+            }
+          };
+          // a page's factors: of one that the row does not see at all they are
+          // harmless ones, whatever its scales
+          auto factors = [&](int page) {
+            float4 f = sc[page];
+            if (kMasked && page * kPage > lim) f = make_float4(1.f, 0.f, 1.f, 0.f);
+            f.x = max_nan(f.x * cf, kKv8MinScale);  // positive: -inf stays -inf
+            return f;
+          };
+          float mx = kNone;
+          auto top = [&](uint32_t (&v)[16], int page) {
+            mask(v, page);
+            auto at = [&](int e) { return __uint_as_float(v[e]); };
             float g = max3(at(0), at(1), at(2));
 #pragma unroll
             for (int e = 3; e < 15; e += 2) g = max3(g, at(e), at(e + 1));
             g = fmaxf(g, at(15));
-            const float4 f = factors(half * (kPagesPerStep / 2) + page);
+            const float4 f = factors(page);
             mx = fmaxf(mx, fmaf(g, f.x, f.y));
+          };
+          load(r1, kPagesPerStep - 1);
+#pragma unroll(kMasked ? 1 : kTurnsMax)
+          for (int page = kPagesPerStep - 2; page >= 0; page -= 2) {
+            tmem_wait_ld(r1);
+            load(r0, page);
+            top(r1, page + 1);
+            tmem_wait_ld(r0);
+            if (page) load(r1, page - 1);
+            top(r0, page);
           }
-        }
-        // the product before last of this group frees its weights' place and its O
-        if (n) ok = wait(&sm.pvdone[x], (n - 1) & 1);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const bool grow = mx > m + kSlack;
-        if (__any_sync(0xffffffffu, grow)) {
-          const float f = grow ? ex2(m - mx) : 1.f;
-          if (grow) m = mx;
-          l *= f;
-          if (mine) {
-            tc_fence_after();
+          const bool grow = mx > m + kSlack;
+          if (__builtin_expect(__any_sync(0xffffffffu, grow), 0)) {
+            const float f = grow ? ex2(m - mx) : 1.f;
+            if (grow) m = mx;
+            l *= f;
+            if (any) {
 #pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-              uint32_t o[16];
-              tmem_ld16(o, to + 128 * x + 16 * c);
-              tmem_wait_ld();
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t o[16];
+                tmem_ld16(o, to + 128 * x + 16 * c);
+                tmem_wait_ld(o);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st16(to + 128 * x + 16 * c, o);
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st16(to + 128 * x + 16 * c, o);
+              }
+              tmem_wait_st();
             }
-            tmem_wait_st();
           }
-        }
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          load_scores(half);
-#pragma unroll
-          for (int page = 0; page < kPagesPerStep / 2; ++page) {
-            const float4 f = factors(half * (kPagesPerStep / 2) + page);
+          // They take the place of scores that this thread has read: a page's 16 halves
+          // 8 columns from 8 page on.
+          auto weights = [&](uint32_t (&v)[16], int page) {
+            const float4 f = factors(page);
             const uint64_t mul = pack2(f.x, f.x), off = pack2(f.y - m, f.y - m);
             uint64_t sum = 0;
             uint32_t h[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const uint32_t* s2 = &r[page / 2][page % 2 * 16 + 2 * e];
-              const float2 y = unpack2(fma2(pack2(__uint_as_float(s2[0]), __uint_as_float(s2[1])), mul, off));
+              const float2 y = unpack2(fma2(pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), mul, off));
               const float p0 = ex2(y.x), p1 = ex2(y.y);  // weight times V scale
               sum = add2(sum, pack2(p0, p1));
               h[e] = half2_bits(p0, p1);
             }
             const float2 t = unpack2(sum);
             l = fmaf(t.x + t.y, f.z, l);
-            uint8_t* dst = sm.p[x] + half * (kRows * 128);
-            *(uint4*)(dst + word_at(row, 2 * page)) = make_uint4(h[0], h[1], h[2], h[3]);
-            *(uint4*)(dst + word_at(row, 2 * page + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
+            tmem_st8(ts + 8 * page, h);
+          };
+#pragma unroll(kMasked ? 1 : kTurnsWeights)
+          for (int page = 0; page < kPagesPerStep; page += 2) {
+            if (page) {
+              tmem_wait_ld(r0);
+              mask(r0, page);
+            }
+            load(r1, page + 1);
+            weights(r0, page);
+            tmem_wait_ld(r1);
+            if (page + 2 < kPagesPerStep) load(r0, page + 2);
+            mask(r1, page + 1);
+            weights(r1, page + 1);
           }
-        }
-        fence_async_shared();
-        tc_fence_before();
-        mbar_arrive(&sm.pfull[x]);
-        ++mine;
-        ++n;
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&sm.pfull[x]);
+          any = true;
+          odd ^= 1;
+        };
+        if (j >= first_masked) work(std::true_type{});
+        else work(std::false_type{});
       }
-      if (ok && mine) ok = wait(&sm.pvdone[x], (n - 1) & 1);  // the group's last product
+      if (ok && any) ok = wait(&sm.pvdone[x], odd ^ 1);  // the group's last product
       ok = __all_sync(0xffffffffu, ok);
       sm.ml[x][row] = make_float2(m, l);
       softmax_sync();
@@ -754,75 +803,60 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
         fB = ex2(mlB.x - mj);
         ml = make_float2(mj, mlA.y * fA + mlB.y * fB);
       }
-      softmax_sync();
       const bool hasA = TWO ? x == 0 : cnt > 1 || ((j - 1) & 1) == 0, hasB = TWO ? x == 1 : cnt > 1 || ((j - 1) & 1) == 1;
       const bool starts = w.p == 0, ends = w.p + cnt == w.steps;
-      const long long ub = u0 + (units - left) - w.p;
+      const int share = sm.share;
+      const long long ub = (long long)blockIdx.x * share + (units - left) - w.p;
       const int c0 = (int)(ub / share), pieces = (int)((ub + w.steps - 1) / share) - c0 + 1;
-      if (starts && ends) ml.y = 1.f / ml.y;
-      sm.ml[x][row] = ml;
-      constexpr int kTile = TWO ? 2 * kRows : kRows;
-      auto write = [&](int r, int y, float4 v, float inv_sum) {
-        const int rq = row_of(r);
-        uint16_t* o = a.out + (int64_t)(w.s.r0 + row0 + rq) * a.out_stride + (size_t)(w.h * a.group + r - rq * a.group) * D + 4 * y;
-        *(uint2*)o = make_uint2(f2bf(v.x * inv_sum) | (uint32_t)f2bf(v.y * inv_sum) << 16,
-                                f2bf(v.z * inv_sum) | (uint32_t)f2bf(v.w * inv_sum) << 16);
+      // Columns jd D/4 + y of O hold dim 4 y + jd: a thread takes 16 dims of its row at
+      // a time (groups on the same rows: half of the dims each). Results go through
+      // shared memory as bf16 (row r's 16-byte word y at y ^ (r mod D / 8)), so that a
+      // row is written by neighbouring lanes; a shared tile's partials straight to the
+      // workspace, there [16-byte words][rows].
+      constexpr int kTile = TWO ? 2 * kRows : kRows, kWords = D / 8;
+      const int mine = TWO ? 128 * x + row : row;  // the thread's row of the tile
+      const int at0 = TWO ? 0 : x * (D / 32), at1 = TWO ? D / 16 : at0 + D / 32;
+      auto put = [&](int r, int at, const float4 (&v)[4], float f) {
+        uint8_t* dst = sm.out + r * (2 * D);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          *(uint4*)(dst + (((2 * at + e) ^ (r & (kWords - 1))) << 4)) =
+              make_uint4(bf2_bits(v[2 * e].x * f, v[2 * e].y * f), bf2_bits(v[2 * e].z * f, v[2 * e].w * f),
+                         bf2_bits(v[2 * e + 1].x * f, v[2 * e + 1].y * f), bf2_bits(v[2 * e + 1].z * f, v[2 * e + 1].w * f));
       };
-      // Half of the dims at a time through shared memory (the group's weights'
-      // place), so that a row is written by neighbouring lanes: row r's 16-byte
-      // word y stands at y ^ (r mod D / 8). Columns jd D/4 + y of O hold dim 4 y + jd.
-      constexpr int kHalf = D / 8;
-      float4* tile = (float4*)sm.p[x];
+      auto partial = [&](int slot) { return (float4*)(a.part + (size_t)slot * kTile * kCol); };
+      float4* part = partial(2 * blockIdx.x + starts);
+      const float inv_sum = 1.f / ml.y;
 #pragma unroll 1
-      for (int half = TWO ? 0 : x; half <= (TWO ? 1 : x) && active; ++half) {
-#pragma unroll 1
-        for (int y0 = 0; y0 < kHalf; y0 += 8) {
-          float o[4][8];
+      for (int at = at0; at < at1 && active; ++at) {
+        uint32_t rA[4][4], rB[4][4];
+#pragma unroll
+        for (int jd = 0; jd < 4; ++jd) {
+          if (hasA) tmem_ld4(rA[jd], to + jd * (D / 4) + 4 * at);
+          if (hasB) tmem_ld4(rB[jd], to + 128 + jd * (D / 4) + 4 * at);
+        }
+        tmem_wait_ld();
+        float4 v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float o[4];
 #pragma unroll
           for (int jd = 0; jd < 4; ++jd) {
-            uint32_t rA[8], rB[8];
-            if (hasA) tmem_ld8(rA, to + jd * (D / 4) + half * kHalf + y0);
-            if (hasB) tmem_ld8(rB, to + 128 + jd * (D / 4) + half * kHalf + y0);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              o[jd][e] = 0.f;
-              if (hasA) o[jd][e] = __uint_as_float(rA[e]) * fA;
-              if (hasB) o[jd][e] = fmaf(__uint_as_float(rB[e]), fB, o[jd][e]);
-            }
+            o[jd] = 0.f;
+            if (hasA) o[jd] = __uint_as_float(rA[jd][e]) * fA;
+            if (hasB) o[jd] = fmaf(__uint_as_float(rB[jd][e]), fB, o[jd]);
           }
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            tile[row * kHalf + ((y0 + e) ^ (row & (kHalf - 1)))] = make_float4(o[0][e], o[1][e], o[2][e], o[3][e]);
+          v[e] = make_float4(o[0], o[1], o[2], o[3]);
         }
-        group_sync(x);
-        constexpr int E = 4, kStep = 4 * (32 / kHalf);  // rows of a lane at once, rows of the group's warps
-        const int y = lane % kHalf, last = min(kRows, cols - (TWO ? 128 * x : 0));
-#pragma unroll 1
-        for (int r1 = (warp & 3) * (32 / kHalf) + lane / kHalf; r1 < last; r1 += E * kStep) {
-          float4 v[E];
-          float2 m2[E];
+        if (starts && ends) {
+          put(mine, at, v, inv_sum);
+        } else if (mine < cols) {
 #pragma unroll
-          for (int k = 0; k < E; ++k) {
-            const int rl = (r1 + k * kStep) % kRows;
-            v[k] = tile[rl * kHalf + (y ^ (rl & (kHalf - 1)))];
-            m2[k] = sm.ml[x][rl];
-          }
-#pragma unroll
-          for (int k = 0; k < E; ++k) {
-            const int rl = r1 + k * kStep, r = TWO ? 128 * x + rl : rl;
-            if (rl >= last) continue;
-            if (starts && ends) {
-              write(r, half * kHalf + y, v[k], m2[k].y);
-            } else {
-              float* part = a.part + ((size_t)(2 * blockIdx.x + starts) * kTile + r) * kCol;
-              *(float4*)(part + 4 * (half * kHalf + y)) = v[k];
-              if (y == 0) *(float2*)(part + D) = m2[k];
-            }
-          }
+          for (int e = 0; e < 4; ++e) part[(4 * at + e) * kTile + mine] = v[e];
+          if (at == 0) ((float2*)(part + D / 4 * kTile))[mine] = ml;
         }
-        group_sync(x);
       }
+      bool write = true;
       if (!(starts && ends)) {
         __threadfence();
         softmax_sync();
@@ -831,43 +865,53 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
           if (sm.flag) a.arrived[c0] = 0;  // ready for the next call
         }
         softmax_sync();
-        if (sm.flag) {
+        write = sm.flag;
+        if (write) {  // the last to arrive joins the tile's partials, in their order
           __threadfence();
-          for (int r = warp; r < cols; r += kSoftmaxThreads / 32) {
-            auto partial = [&](int i) { return a.part + ((size_t)(2 * (c0 + i) + (i == 0)) * kTile + r) * kCol; };
-            float mm = kNone, ss = 0.f;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int i0 = 0; i0 < pieces; i0 += 32) {
-              const int i = i0 + lane;
-              const float2 ml = i < pieces ? __ldcg((const float2*)(partial(i) + D)) : make_float2(kNone, 0.f);
-              const float nm = fmaxf(mm, warp_max(ml.x)), f0 = ex2(mm - nm), f1 = ex2(ml.x - nm);
-              mm = nm;
-              ss = ss * f0 + warp_sum(ml.y * f1);
-              v = make_float4(v.x * f0, v.y * f0, v.z * f0, v.w * f0);
-              for (int k = 0; k < 32 && i0 + k < pieces; k += 4) {
-                float4 y[4];
+          auto of = [&](int i) { return partial(2 * (c0 + i) + (i == 0)); };
+#pragma unroll 1
+          for (int item = tid; item < cols * (D / 16); item += kSoftmaxThreads) {
+            const int at = item / cols, r = item - at * cols;
+            auto sums = [&](int i) { return __ldcg((const float2*)(of(i) + D / 4 * kTile) + r); };
+            float mj = kNone, sum = 0.f;
+#pragma unroll 4
+            for (int i = 0; i < pieces; ++i) mj = fmaxf(mj, sums(i).x);
+            float4 v[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-                  if (lane < D / 4 && i0 + k + e < pieces) y[e] = __ldcg((const float4*)(partial(i0 + k + e) + 4 * lane));
-                }
+            for (int e = 0; e < 4; ++e) v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+            for (int i = 0; i < pieces; ++i) {
+              const float2 y = sums(i);
+              const float f = ex2(y.x - mj);
+              sum += y.y * f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) axpy(v, y[e], __shfl_sync(0xffffffffu, f1, k + e));
-              }
+              for (int e = 0; e < 4; ++e) axpy(v[e], __ldcg(of(i) + (4 * at + e) * kTile + r), f);
             }
-            if (lane < D / 4) write(r, lane, v, 1.f / ss);
+            put(r, at, v, 1.f / sum);
           }
+        }
+      }
+      softmax_sync();
+      if (write) {
+        constexpr int kLanes = D / 4, kOnce = kSoftmaxThreads / kLanes;  // lanes of a row, rows at once
+        const int y = tid % kLanes;
+#pragma unroll 4
+        for (int r = tid / kLanes; r < cols; r += kOnce) {
+          const int rq = row_of(r);
+          uint16_t* o = a.out + (int64_t)(w.s.r0 + row0 + rq) * a.out_stride + (size_t)(w.h * a.group + r - rq * a.group) * D + 4 * y;
+          *(uint2*)o = *(const uint2*)(sm.out + r * (2 * D) + (((y >> 1) ^ (r & (kWords - 1))) << 4) + (y & 1) * 8);
         }
       }
       softmax_sync();  // this tile's maxima and sums have been read
       left -= cnt;
-      w.p += cnt;
-      if (w.p == w.steps) w.next_tile(a);
+      if (tid == 0 && left) sm.at[kSoftmaxPlace].advance(a, cnt);
+      softmax_sync();
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (tid == 0 && sm.failed) set_err(a.c.err, QTTS_DEV_TIMEOUT);
   if (warp == kIssueWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512) : "memory");
 }
