@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
     // cut tiles (reading queries twice, partials out and in: kJoinSteps).
     int total = 0, tiles = 0, most = 0, per = 0, own = 0, lo = 0, share = 0, rows = 0;
     bool whole = false;
-    long long u0 = 0, u1 = 0;
+    int u0 = 0, u1 = 0;
     Kv8Session ses;
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
@@ -312,8 +312,8 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
           tiles += __reduce_add_sync(0xffffffffu, count * a.c.nkv);
           rows += __reduce_add_sync(0xffffffffu, ses.n);
           most = max(most, __reduce_max_sync(0xffffffffu, ses.n ? (ses.L + ses.n + kKeys - 1) / kKeys : 0));
-        } else if (lo <= u0 && u0 < (long long)lo + own) {
-          const int at = (int)(u0 - lo), h = at / per;
+        } else if (lo <= u0 && u0 < lo + own) {
+          const int at = u0 - lo, h = at / per;
           int sum;
           Place& w = sm.at[0];
           w.b = b0 + lane;
@@ -333,16 +333,17 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
         total = carry;
         const int G = gridDim.x;
         share = max((total + G - 1) / G, 4);
-        whole = (long long)((tiles + G - 1) / G) * most <= share + kJoinSteps;
-        u0 = whole ? (long long)tiles * blockIdx.x / G : (long long)blockIdx.x * share;
-        u1 = whole ? (long long)tiles * (blockIdx.x + 1) / G : min(u0 + share, (long long)total);
+        const int each = tiles / G, more = tiles - each * G, me = blockIdx.x;
+        whole = (long long)(each + (more > 0)) * most <= share + kJoinSteps;
+        u0 = whole ? me * each + min(me, more) : me * share;
+        u1 = whole ? u0 + each + (me < more) : min(u0 + share, total);
         if (u0 >= u1) break;
       }
     }
     // key steps of this CTA
     __syncwarp();
     const Place first = sm.at[0];
-    int units = (int)max(u1 - u0, 0ll);
+    int units = max(u1 - u0, 0);
     if (whole && units) {
       Place x = first;
       const int count = units;
@@ -805,9 +806,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
       }
       const bool hasA = TWO ? x == 0 : cnt > 1 || ((j - 1) & 1) == 0, hasB = TWO ? x == 1 : cnt > 1 || ((j - 1) & 1) == 1;
       const bool starts = w.p == 0, ends = w.p + cnt == w.steps;
-      const int share = sm.share;
-      const long long ub = (long long)blockIdx.x * share + (units - left) - w.p;
-      const int c0 = (int)(ub / share), pieces = (int)((ub + w.steps - 1) / share) - c0 + 1;
+      const bool closed = starts && ends;
       // Columns jd D/4 + y of O hold dim 4 y + jd: a thread takes 16 dims of its row at
       // a time (groups on the same rows: half of the dims each). Results go through
       // shared memory as bf16 (row r's 16-byte word y at y ^ (r mod D / 8)), so that a
@@ -848,7 +847,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
           }
           v[e] = make_float4(o[0], o[1], o[2], o[3]);
         }
-        if (starts && ends) {
+        if (closed) {
           put(mine, at, v, inv_sum);
         } else if (mine < cols) {
 #pragma unroll
@@ -857,7 +856,10 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
         }
       }
       bool write = true;
-      if (!(starts && ends)) {
+      if (!closed) {
+        // the tile's first key step, the CTA that has it, and the number of CTAs on the tile
+        const int share = sm.share, ub = blockIdx.x * share + (units - left) - w.p;
+        const int c0 = ub / share, pieces = (ub + w.steps - 1) / share - c0 + 1;
         __threadfence();
         softmax_sync();
         if (tid == 0) {
