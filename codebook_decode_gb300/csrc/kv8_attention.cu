@@ -9,7 +9,7 @@
 // query rows. Codes are exact in half, the blocks' scales are applied outside
 // the products: the K scale (with the softmax scale and log2 e) to the fp32
 // scores, the V scale to the fp32 weights. Weights are rounded to half
-// (2^-12 relative), queries to half after a power of two per column.
+// (2^-11 relative), queries to half after a power of two per column.
 //
 // Softmax: base 2, per-warp running maximum m of score + log2(V scale), so the
 // weights p * s_v that enter the product stay below 2^kSlack whatever the
@@ -36,7 +36,11 @@ namespace qtts {
 namespace {
 
 constexpr int kWaitTries = 1 << 20;  // bound of each wait for a copy (a try suspends for microseconds)
-constexpr int kMaxCols = 32;
+// Columns of a tile, at most; calls with more go to the tcgen05 kernel. Measured on both
+// sides: 32 columns (16 rows, 2 q heads a kv head) behind 100 tokens 16.8 us here, 9.1
+// there, 32 sessions of them behind 8000 295 and 220; 16 columns 8.5 (8 sessions, 100
+// tokens) and 9.4, 110 (32 sessions, 8000) and 219.
+constexpr int kMaxCols = 16;
 // A tile of up to kWholePages pages goes to one CTA when there are enough CTAs
 // for all tiles, up to kWholePagesMany when the tiles take half of the CTAs:
 // joining pieces through global memory costs more than reading the tile with
@@ -46,8 +50,8 @@ constexpr int kTiles = 8;  // tiles whose queries a CTA prepares at a time, at m
 
 // warps of a CTA, CTAs of an SM, copies in flight per warp (blocks of 32 D bytes)
 __host__ __device__ constexpr int warps_of(int NT) { return NT == 1 ? 8 : 4; }
-__host__ __device__ constexpr int ctas_of(int NT) { return NT == 1 ? 2 : NT == 2 ? 2 : 1; }
-__host__ __device__ constexpr int slots_of(int D, int NT) { return (NT == 4 ? 5 : NT == 2 ? 3 : 2) * (128 / D); }
+constexpr int kCtas = 2;
+__host__ __device__ constexpr int slots_of(int D, int NT) { return (NT == 2 ? 3 : 2) * (128 / D); }
 
 struct Session {
   int r0, n, L;
@@ -63,7 +67,7 @@ __host__ __device__ constexpr int query_stride(int D) { return 2 * D + 16; }  //
 __host__ __device__ inline Layout layout(int D, int NT, int cols, int B) {
   Layout l;
   const int W = warps_of(NT), S = slots_of(D, NT);
-  l.tiles = NT == 4 ? 2 : cols <= 4 ? kTiles : 4;
+  l.tiles = cols <= 4 ? kTiles : 4;
   l.part = W * S * 32 * D;
   l.bar = l.part + W * cols * (D + 4) * 4;  // floats of one column: values, maximum, sum, 2 unused
   l.query = l.bar + W * S * 8;
@@ -136,7 +140,7 @@ struct Tile {
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(warps_of(NT) * 32, ctas_of(NT)) attention_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(warps_of(NT) * 32, kCtas) attention_kernel(const __grid_constant__ Args a) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   constexpr int W = warps_of(NT), kSlots = slots_of(D, NT);
   constexpr int KC = D / 64;  // 64-dim chunks of a K row
@@ -696,7 +700,7 @@ cudaError_t launch_one(const Args& a, int sms, cudaStream_t s) {
   cudaLaunchConfig_t lc{};
   cudaLaunchAttribute at[1];
   early_launch(lc, at);
-  lc.gridDim = dim3(a.one_each && a.q.bt_stride <= kWholePages ? a.q.B * a.c.nkv : sms * ctas_of(NT));
+  lc.gridDim = dim3(a.one_each && a.q.bt_stride <= kWholePages ? a.q.B * a.c.nkv : sms * kCtas);
   lc.blockDim = dim3(32 * warps_of(NT));
   lc.dynamicSmemBytes = layout(D, NT, a.max_cols, a.q.B).bytes;
   lc.stream = s;
@@ -709,16 +713,16 @@ cudaError_t kv8_attention_setup(int d) {
   cudaError_t e = kv8_chunk_setup(d);
   if (e != cudaSuccess) return e;
   if (d == 64) {
-    (e = setup_one<64, 1>()) || (e = setup_one<64, 2>()) || (e = setup_one<64, 4>());
+    (e = setup_one<64, 1>()) || (e = setup_one<64, 2>());
   } else {
-    (e = setup_one<128, 1>()) || (e = setup_one<128, 2>()) || (e = setup_one<128, 4>());
+    (e = setup_one<128, 1>()) || (e = setup_one<128, 2>());
   }
   return e;
 }
 
 // the arrival counts, then two partial tiles for each CTA of the largest grid
 size_t kv8_attention_workspace(int d, int sms) {
-  const size_t ctas = 2 * (size_t)sms;
+  const size_t ctas = kCtas * (size_t)sms;
   return ctas * sizeof(unsigned) + std::max(2 * ctas * kMaxCols * (d + 4) * sizeof(float), kv8_chunk_workspace(d, sms));
 }
 
@@ -732,18 +736,18 @@ bool kv8_attention_fits(const Kv8View& v, const Kv8Batch& q, int group) {
 
 cudaError_t kv8_attention(const Kv8View& v, const Kv8Batch& q, int d, int group, int sms, const uint16_t* qp,
                           int64_t q_stride, float scale, uint16_t* out, int64_t out_stride, void* work, cudaStream_t s) {
-  // the fewest n-tiles that hold every session's columns; more rows go in tiles of 32 columns
+  // the fewest n-tiles that hold every session's columns
   const long long cols = (long long)q.max_new * group;
-  float* part = (float*)((char*)work + 2 * (size_t)sms * sizeof(unsigned));
+  float* part = (float*)((char*)work + kCtas * (size_t)sms * sizeof(unsigned));
   if (cols > kMaxCols)
     return kv8_chunk(v, q, d, group, sms, qp, q_stride, scale, out, out_stride, (unsigned*)work, part, s);
-  const int nt = cols <= 8 ? 1 : cols <= 16 ? 2 : 4;
+  const int nt = cols <= 8 ? 1 : 2;
   Args a{};
   a.c = v;
   a.q = q;
   a.group = group;
   a.max_cols = (int)cols;
-  a.one_each = (long long)q.B * v.nkv <= sms * ctas_of(nt);
+  a.one_each = (long long)q.B * v.nkv <= sms * kCtas;
   a.qp = qp;
   a.q_stride = q_stride;
   a.scale_log2 = scale * kLog2e;
@@ -752,8 +756,8 @@ cudaError_t kv8_attention(const Kv8View& v, const Kv8Batch& q, int d, int group,
   a.arrived = (unsigned*)work;
   a.part = part;
   if (d == 64)
-    return nt == 1 ? launch_one<64, 1>(a, sms, s) : nt == 2 ? launch_one<64, 2>(a, sms, s) : launch_one<64, 4>(a, sms, s);
-  return nt == 1 ? launch_one<128, 1>(a, sms, s) : nt == 2 ? launch_one<128, 2>(a, sms, s) : launch_one<128, 4>(a, sms, s);
+    return nt == 1 ? launch_one<64, 1>(a, sms, s) : launch_one<64, 2>(a, sms, s);
+  return nt == 1 ? launch_one<128, 1>(a, sms, s) : launch_one<128, 2>(a, sms, s);
 }
 
 }  // namespace qtts
