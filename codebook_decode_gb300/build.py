@@ -29,6 +29,7 @@ def _stale(obj, src):
         return True
     deps = [src, os.path.join(CSRC, "qtts_internal.h"), os.path.join(CSRC, "device_util.cuh"),
             os.path.join(CSRC, "kv8.cuh"), os.path.join(CSRC, "kv8_attn.cuh"),
+            os.path.join(CSRC, "tcgen05.cuh"),
             os.path.join(ROOT, "include", "qtts.h")]
     return any(os.path.getmtime(d) > os.path.getmtime(obj) for d in deps)
 

@@ -37,6 +37,7 @@
 
 #include "kv8.cuh"
 #include "kv8_attn.cuh"
+#include "tcgen05.cuh"
 
 namespace qtts {
 namespace {
@@ -59,14 +60,6 @@ constexpr int kTurnsMax = 2, kTurnsWeights = 4;
 constexpr int kIssueWarp = (kSoftmaxThreads + kWidenThreads) / 32;
 constexpr int kPlaces = kWidenThreads / 32 + 2, kIssuePlace = kPlaces - 2, kSoftmaxPlace = kPlaces - 1;
 
-// Operands in shared memory: rows of 64 halves (128 bytes), rows one after the
-// other, 64-wide blocks of columns one after the other, and in a row the 16-byte
-// words exchanged by the row's low bits (the tensor cores' 128-byte swizzle), so
-// that neither a row's words nor a word of neighbouring rows share banks.
-__device__ __forceinline__ int word_at(int row, int word) { return row * 128 + ((word ^ (row & 7)) << 4); }
-__device__ __forceinline__ uint64_t swizzled_desc(const void* p) {
-  return (uint64_t)((smem_addr(p) >> 4) & 0x3FFFu) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
-}
 // of the 16 columns (of k) number ks: their place in units of 16 bytes
 __host__ __device__ constexpr uint64_t k_step(int ks, int rows) { return (ks / 4 * rows * 128 + ks % 4 * 32) / 16; }
 
@@ -174,7 +167,6 @@ __device__ __forceinline__ void load_if(float2& v, const void* p, bool yes) {
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
-__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void softmax_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
 }
@@ -200,20 +192,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
-  return p != 0;
-}
 constexpr uint32_t idesc_f16(int M, int N) {  // kind::f16: fp32 accumulator, half A and B, both K-major
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-__device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t at) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(at));
 }
 __device__ __forceinline__ void tmem_st8(uint32_t at, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(r[0]), "r"(r[1]),
@@ -231,13 +211,6 @@ __device__ __forceinline__ void tmem_ld4(uint32_t (&r)[4], uint32_t at) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(at));
-}
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-// the same, for the registers of a load that was asked for earlier: their use stays behind it
-__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
-                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
 // A from tensor memory: a row's halves two to a column
 __device__ __forceinline__ void tc_mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {

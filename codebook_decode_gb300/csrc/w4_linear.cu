@@ -27,6 +27,7 @@
 
 #include "device_util.cuh"
 #include "qtts_internal.h"
+#include "tcgen05.cuh"
 
 struct qtts_w4 {
   int N = 0, K = 0, group = 0, device = 0, G = 0;
@@ -193,7 +194,7 @@ __device__ __forceinline__ void copy16(void* dst, const void* src) {
 // tiles at a time) while the first weights are on their way; without it every
 // k tile waited for its activations.
 template <int NT, int R>
-__global__ void __launch_bounds__(kW4Threads, NT == 1 ? 3 : NT <= 2 ? 2 : 1) w4_kernel(const __grid_constant__ W4Args a) {
+__global__ void __launch_bounds__(kW4Threads, NT == 1 ? 3 : NT <= 4 ? 2 : 1) w4_kernel(const __grid_constant__ W4Args a) {
   extern __shared__ __align__(16) uint8_t w4_smem[];  // activations, then the sums [k warps][8 NT][rows + 4]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   cg::cluster_group cluster = cg::this_cluster();
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 3 : NT <= 2 ? 2 : 1) w4_
   int row_at[NT];  // a column's activation row (beyond M any: it is not written)
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) row_at[nt] = min(nt * 8 + g, a.M - 1) * pitch;
-  constexpr int P = R == 1 ? 6 : NT == 4 ? 6 : 4;  // tiles in flight
+  constexpr int P = R == 1 ? 6 : 4;  // tiles in flight
   uint4 w[P][R];
   uint2 sc[P][R];
   for (int c0 = t0; c0 < t1; c0 += a.chunk) {
@@ -349,6 +350,193 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 3 : NT <= 2 ? 2 : 1) w4_
   cluster.sync();  // no CTA leaves while another reads its sums
 }
 
+// ---- more rows, on the tcgen05 tensor cores
+//
+// A CTA takes 128 weight rows (16 a warp) and all activation rows as NCOL columns, a k
+// tile of 64 at a time: codes widened to bf16 and activations in shared
+// memory with the 128-byte swizzle, a group's partial sums in tensor memory. Two tiles
+// later, when their product has run, every warp takes half of its rows' columns, times
+// the group's scale, into fp32 registers. CTAs of a cluster split k as above.
+//
+// Tensor memory: a CTA's four (or fewer) accumulators take 4 NCOL of the 512 columns,
+// and shared memory is asked for so that an SM holds two CTAs at most: an allocation
+// never waits for a CTA that waits for this one.
+//
+// 64 x 12288 x 2048 23 us against 29 of the kernel above, 48 x 30000 x 4096 64 against
+// 97: bound by the chain of a tile (product, sums, codes, barrier: 0.8 us), which two
+// CTAs an SM overlap.
+constexpr int kTcRows = 128, kTcTries = 1 << 17, NCOL = kW4MaxM;
+constexpr int kTcSmem = 80 * 1024;
+__global__ void __launch_bounds__(kW4Threads, 2) w4_tc_kernel(const __grid_constant__ W4Args a) {
+  extern __shared__ __align__(1024) uint8_t w4_tc_smem[];  // [2] weights, [4] activations; then the sums
+  __shared__ uint64_t bars[2];                             // the products of even, odd tiles have run
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_failed;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int S = 1 << a.s_log, rank = blockIdx.x & (S - 1), cta = blockIdx.x >> a.s_log;
+  const int unit_log = a.group == 128 ? 1 : 0;  // k tiles of a group
+  const bool fine = a.group == 32;
+  const int units = a.KT >> unit_log;
+  const int t0 = (units * rank >> a.s_log) << unit_log, n = ((units * (rank + 1) >> a.s_log) << unit_log) - t0;
+  uint8_t* const wts = w4_tc_smem;
+  uint8_t* const act = w4_tc_smem + 2 * kTcRows * 128;
+
+  if (tid == 0) {
+    mbar_init(&bars[0], 1);
+    mbar_init(&bars[1], 1);
+    mbar_init_fence();
+    s_failed = 0;
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s_tmem)), "n"(4 * NCOL)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  // this warp's codes, four tiles ahead; the scales of a thread's row, two tiles ahead of their use
+  const int rb = cta * 8 + warp, row = (warp & 3) * 32 + lane;
+  const uint4* codes = a.codes + ((size_t)min(rb, a.RB - 1) * a.KT + t0) * 32 + lane;
+  const int rbs = min(cta * 8 + row / 16, a.RB - 1);
+  const uint16_t* scales = a.scales + (fine ? ((size_t)rbs * a.sunits + t0) * 32 + scale_slot(row & 15, 0, 32)
+                                            : ((size_t)rbs * a.sunits + (t0 >> unit_log)) * 16 + scale_slot(row & 15, 0, 64));
+  uint4 w[4];
+  uint32_t sc[4] = {0u, 0u, 0u, 0u};
+  auto load_scale = [&](uint32_t& v, int i) {
+    if (i < n) v = fine ? *(const uint32_t*)(scales + i * 32) : scales[(i >> unit_log) * 16];
+  };
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < n) w[i] = load_stream(codes + i * 32);
+  load_scale(sc[0], 0);
+  load_scale(sc[1], 1);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  grid_dependency_wait();  // activations
+
+  auto load_act = [&](int i) {  // tile i's activations, 16 bytes are 8 k; zeros beyond M and K
+#pragma unroll
+    for (int e = 0; e < NCOL * 8 / kW4Threads; ++e) {
+      const int idx = e * kW4Threads + tid, m = idx >> 3, word = idx & 7, k = (t0 + i) * kW4K + word * 8;
+      const bool in = i < n && m < a.M && k < a.K;
+      const uint16_t* src = in ? a.x + (int64_t)m * a.x_stride + k : a.x;
+      if (i < n)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(act + (i & 3) * (NCOL * 128) + word_at(m, word))),
+                     "l"(src), "r"(in ? 16 : 0)
+                     : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // bounded; a product that does not end gives NaN
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (mbar_test(bar, parity)) return;
+#pragma unroll 1
+    for (int tries = 0; tries < kTcTries && !*(volatile int*)&s_failed; ++tries)
+      if (mbar_test_sleep(bar, parity, 10000)) return;
+    *(volatile int*)&s_failed = 1;
+  };
+  load_act(0);
+  load_act(1);
+  constexpr int kCols = NCOL / 2;  // of a thread
+  float acc[kCols];
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
+  const uint32_t mine = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (warp >> 2) * kCols;
+  auto accumulator = [&](int i, int half) { return (fine ? 2 * (i & 1) + half : i >> unit_log & 1) * NCOL; };
+  auto add = [&](int i, int half, float s) {
+#pragma unroll
+    for (int c0 = 0; c0 < kCols; c0 += 16) {
+      uint32_t v[16];
+      tmem_ld16(v, mine + accumulator(i, half) + c0);
+      tmem_wait_ld(v);
+#pragma unroll
+      for (int c = 0; c < 16; ++c) acc[c0 + c] = fmaf(__uint_as_float(v[c]), s, acc[c0 + c]);
+    }
+  };
+#pragma unroll 1
+  for (int i0 = 0; i0 < n + 2; i0 += 4) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u;
+      if (i >= n + 2) break;
+      if (i >= 2) {  // tile i - 2 has run: its places are free, its sums are there
+        wait(&bars[i & 1], ((i >> 1) - 1) & 1);
+        tc_fence_after();
+        const uint32_t s2 = sc[(u + 2) & 3];
+        if (fine) {
+          add(i - 2, 0, bf2f(s2 & 0xffffu));
+          add(i - 2, 1, __uint_as_float(s2 & 0xffff0000u));
+        } else if (!unit_log || (i & 1)) {
+          add(i - 2, 0, bf2f(s2));
+        }
+      }
+      load_scale(sc[(u + 2) & 3], i + 2);
+      if (i >= n) continue;
+      load_act(i + 2);
+      const uint32_t words[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+      uint8_t* dst = wts + (i & 1) * (kTcRows * 128);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          *(uint4*)(dst + word_at(warp * 16 + 8 * r + g, 4 * h + t)) =
+              make_uint4(widen4(words[2 * h] >> 4 * r), widen4(words[2 * h] >> (4 * r + 8)), widen4(words[2 * h + 1] >> 4 * r),
+                         widen4(words[2 * h + 1] >> (4 * r + 8)));
+      if (i + 4 < n) w[u] = load_stream(codes + (i + 4) * 32);
+      asm volatile("cp.async.wait_group 2;" ::: "memory");
+      fence_async_shared();
+      tc_fence_before();
+      __syncthreads();
+      if (warp == 0) {
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t ad = swizzled_desc(dst), bd = swizzled_desc(act + (i & 3) * (NCOL * 128));
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            tc_mma(tmem + accumulator(i, ks >> 1), ad + 2 * ks, bd + 2 * ks, tc_idesc_bf16(kTcRows, NCOL),
+                   fine ? ks & 1 : ks > 0 || (unit_log && (i & 1)));
+          tc_commit(&bars[i & 1]);
+        }
+        __syncwarp();
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(4 * NCOL) : "memory");
+  const float poison = s_failed ? __int_as_float(0x7fffffff) : 0.f;
+  const int n0 = cta * kTcRows;
+  auto put = [&](int m, int r, float v) {
+    if (m < a.M && n0 + r < a.N) {
+      if (a.y_f32) ((float*)a.y)[(int64_t)m * a.y_stride + n0 + r] = v;
+      else ((uint16_t*)a.y)[(int64_t)m * a.y_stride + n0 + r] = f2bf(v);
+    }
+  };
+  float* part = (float*)w4_tc_smem;  // [NCOL][rows + 4]
+  constexpr int kPitch = kTcRows + 4;
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) {
+    const int m = (warp >> 2) * kCols + c;
+    if (S == 1) put(m, row, acc[c] + poison);
+    else part[m * kPitch + row] = acc[c] + poison;
+  }
+  if (S == 1) return;
+  cluster.sync();
+#pragma unroll 1
+  for (int idx = rank * kW4Threads + tid; idx < kTcRows * a.M; idx += S * kW4Threads) {
+    const int m = idx / kTcRows, r = idx % kTcRows;
+    float v[kW4MaxSplit];
+#pragma unroll
+    for (int c = 0; c < kW4MaxSplit; ++c) v[c] = c < S ? cluster.map_shared_rank(part, c)[m * kPitch + r] : 0.f;
+#pragma unroll
+    for (int c = 1; c < kW4MaxSplit; ++c) v[0] += v[c];
+    put(m, r, v[0]);
+  }
+  cluster.sync();  // no CTA leaves while another reads its sums
+}
+
 constexpr int kW4Smem = 200 * 1024;  // at most
 
 template <int NT, int R>
@@ -357,7 +545,9 @@ cudaError_t w4_setup_one() {
 }
 cudaError_t w4_setup() {
   cudaError_t e;
-  (e = w4_setup_one<1, 1>()) || (e = w4_setup_one<2, 2>()) || (e = w4_setup_one<4, 2>()) || (e = w4_setup_one<8, 2>());
+  (e = w4_setup_one<1, 1>()) || (e = w4_setup_one<2, 1>()) || (e = w4_setup_one<2, 2>()) || (e = w4_setup_one<4, 1>()) ||
+      (e = w4_setup_one<8, 2>()) ||
+      (e = cudaFuncSetAttribute(w4_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem));
   return e;
 }
 
@@ -377,6 +567,24 @@ cudaError_t w4_launch(W4Args a, cudaStream_t s) {
   lc.numAttrs = 1;
   early_launch(lc, at);
   return cudaLaunchKernelEx(&lc, w4_kernel<NT, R>, a);
+}
+
+cudaError_t w4_tc_launch(W4Args a, int sms, cudaStream_t s) {
+  const int ctas = (a.RB + 7) / 8;
+  a.s_log = 0;
+  while ((1 << a.s_log) < kW4MaxSplit && ctas << a.s_log < sms && a.KT >= 8 << a.s_log) ++a.s_log;
+  cudaLaunchConfig_t lc{};
+  lc.gridDim = dim3(ctas << a.s_log);
+  lc.blockDim = dim3(kW4Threads);
+  lc.dynamicSmemBytes = kTcSmem;
+  lc.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 1 << a.s_log;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  lc.numAttrs = 1;
+  early_launch(lc, at);
+  return cudaLaunchKernelEx(&lc, w4_tc_kernel, a);
 }
 
 char g_w4_err[256];
@@ -546,14 +754,31 @@ int qtts_w4_linear(qtts_w4* w, int M, const uint16_t* x, int64_t x_stride, void*
   const cudaStream_t s = (cudaStream_t)stream;
   // Up to 8 rows: 16 weight rows a CTA, its warps along k (activations are few,
   // weights spread over all SMs), 32 where that fills the SMs four times over
-  // (12288 x 2048: 6.7 us against 7.5). More rows: 64 weight rows a CTA, so that
-  // fewer CTAs copy the activations. Clusters along k until the SMs have a CTA
-  // each and while every warp keeps two k tiles.
-  a.rw_log = M <= 8 ? w->RB > 4 * w->G : 1;
-  const int ctas = M <= 8 ? w->RB >> a.rw_log : (w->RB + 3) / 4, kw = kW4Warps >> a.rw_log;
-  while ((1 << a.s_log) < kW4MaxSplit && ctas << a.s_log < w->G && w->KT >= (4 * kw) << a.s_log) ++a.s_log;
+  // (12288 x 2048: 6.7 us against 7.5). More rows: every CTA copies all
+  // activations, so as many of its warps along the weight rows as leave about one
+  // CTA an SM (24 x 9000 x 4096: 14 us with 4 warps, 18 with 2; 16 x 30000 x 4096
+  // 38 with 8, 61 with 2 or 4), and one row block a warp, two where there are few
+  // activations and many blocks (12 x 2048 x 6144: 5.9 us with one, 8.1 with two;
+  // 16 x 30000 x 4096 80 and 38). Clusters along k until the SMs have a CTA each
+  // and while every warp keeps two k tiles. Over 32 rows the tcgen05 kernel where
+  // its clusters can fill three quarters of the SMs (64 x 4096 x 2048: 12.9 us
+  // against 15.5; 64 x 2048 x 6144: 26 against 12.7).
+  const int blocks = M <= 8 ? 1 : M <= 16 ? 1 + (w->RB > 2 * w->G) : M <= 32 ? 1 : 2;  // row blocks of a warp
+  auto ctas_of = [&](int rw_log) { return (w->RB + (blocks << rw_log) - 1) / (blocks << rw_log); };
+  if (M <= 8) {
+    a.rw_log = w->RB > 4 * w->G;
+  } else {
+    a.rw_log = 1;
+    const int most = M <= 16 ? w->G * 13 / 10 : M <= 32 ? w->G : 1 << 30;
+    while (a.rw_log < 3 && ctas_of(a.rw_log) > most) ++a.rw_log;
+  }
+  const int kw = kW4Warps >> a.rw_log;
+  while ((1 << a.s_log) < kW4MaxSplit && ctas_of(a.rw_log) << a.s_log < w->G && w->KT >= (4 * kw) << a.s_log) ++a.s_log;
   if (M <= 8) e = w4_launch<1, 1>(a, s);
-  else e = M <= 16 ? w4_launch<2, 2>(a, s) : M <= 32 ? w4_launch<4, 2>(a, s) : w4_launch<8, 2>(a, s);
+  else if (M <= 16) e = blocks == 1 ? w4_launch<2, 1>(a, s) : w4_launch<2, 2>(a, s);
+  else if (M <= 32) e = w4_launch<4, 1>(a, s);
+  else if (4 * ((w->RB + 7) / 8 * kW4MaxSplit) >= 3 * w->G) e = w4_tc_launch(a, w->G, s);
+  else e = w4_launch<8, 2>(a, s);
   if (e != cudaSuccess) {
     cudaGetLastError();  // reported here, not by the caller's next CUDA call
     return fail(w, QTTS_E_CUDA, "qtts_w4_linear: %s", cudaGetErrorString(e));

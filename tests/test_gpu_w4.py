@@ -177,3 +177,74 @@ def bf16_twice(L, a, N):
     qtts.qtts_w4_linear(L.w, 4, a, N, y, N, qtts.QTTS_DTYPE_BF16)
     torch.cuda.synchronize()
     return y.double().cpu().numpy()
+
+
+@pytest.mark.parametrize("M,N,K,group", [
+    (33, 3700, 32, 32), (64, 3700, 32 * 45, 32), (40, 20001, 32 * 6, 32),     # k tiles that end half full
+    (64, 3700, 64, 64), (48, 4999, 64 * 33, 64), (64, 20001, 64 * 5, 64),
+    (33, 3700, 128, 128), (64, 4999, 128 * 17, 128), (64, 20001, 128 * 3, 128),
+    (12, 6001, 64 * 20, 64), (16, 30001, 64 * 3, 64), (24, 6001, 128 * 9, 128), (32, 12289, 32 * 33, 32)])
+def test_many_rows_of_weights(M, N, K, group):
+    """The variants of large layers, with strided rows and rows behind the last left as they were."""
+    rng = np.random.default_rng(N + K + M)
+    q = rng.integers(-8, 8, (N, K)).astype(np.int8)
+    sb, s = bf16(np.exp(rng.standard_normal((N, K // group))))
+    xb, x = bf16(rng.standard_normal((M + 1, K + 8)))
+    xb = xb.copy()
+    xb[:, K:] = 0x7FC0  # between the rows, and behind the last: not read
+    xb[M] = 0x7FC0
+    with Linear(N, K, group) as L:
+        qtts.qtts_w4_load(L.w, q, sb)
+        d = bits(xb)
+        for f32 in (0, 1):
+            y = torch.full((M + 1, N + 3), 7.0, dtype=torch.float32 if f32 else torch.bfloat16, device="cuda")
+            for _ in range(2):
+                qtts.qtts_w4_linear(L.w, M, d, K + 8, y, N + 3, qtts.QTTS_DTYPE_F32 if f32 else qtts.QTTS_DTYPE_BF16)
+            y = y.double().cpu().numpy()
+            assert (y[M] == 7).all() and (y[:, N:] == 7).all()
+            check(y[:M, :N], x[:M, :K], q, s, group, f32)
+
+
+def test_non_finite_values_of_many_rows_stay_in_their_row_and_group():
+    rng = np.random.default_rng(16)
+    N, K = 3700, 256
+    q = rng.integers(-8, 8, (N, K)).astype(np.int8)
+    sb, _ = bf16(np.exp(rng.standard_normal((N, K // 64))))
+    sb = sb.copy()
+    sb[133, 2] = 0x7FC0
+    xb, _ = bf16(rng.standard_normal((50, K)))
+    xb = xb.copy()
+    xb[17, 5] = 0x7FC0
+    with Linear(N, K, 64) as L:
+        qtts.qtts_w4_load(L.w, q, sb)
+        y = torch.zeros(50, N, device="cuda")
+        qtts.qtts_w4_linear(L.w, 50, bits(xb), K, y, N, qtts.QTTS_DTYPE_F32)
+        y = y.cpu().numpy()
+        assert np.isnan(y[17]).all() and np.isnan(y[:, 133]).all()
+        assert np.isfinite(np.delete(np.delete(y, 17, 0), 133, 1)).all()
+
+
+def test_large_products_on_two_streams_and_in_a_graph():
+    rng = np.random.default_rng(17)
+    N, K = 5000, 512
+    q = rng.integers(-8, 8, (N, K)).astype(np.int8)
+    sb, s = bf16(np.exp(rng.standard_normal((N, K // 128))))
+    xb, x = bf16(rng.standard_normal((64, K)))
+    with Linear(N, K, 128) as L:
+        qtts.qtts_w4_load(L.w, q, sb)
+        d, f32 = bits(xb), qtts.QTTS_DTYPE_F32
+        y = [torch.zeros(64, N, device="cuda") for _ in range(3)]
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        torch.cuda.synchronize()
+        for _ in range(10):
+            for out, st in zip(y, streams):
+                qtts.qtts_w4_linear(L.w, 64, d, K, out, N, f32, st.cuda_stream)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(4):
+                qtts.qtts_w4_linear(L.w, 64, d, K, y[2], N, f32, torch.cuda.current_stream().cuda_stream)
+        g.replay()
+        torch.cuda.synchronize()
+        check(y[0].double().cpu().numpy(), x, q, s, 128, True)
+        assert torch.equal(y[0], y[1]) and torch.equal(y[0], y[2])
