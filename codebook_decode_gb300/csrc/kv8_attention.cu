@@ -731,12 +731,16 @@ size_t kv8_attention_workspace(int d, int sms) {
   return ctas * sizeof(unsigned) + std::max(2 * ctas * kMaxCols * (d + 4) * sizeof(float), kv8_chunk_workspace(d, sms));
 }
 
+// pages of a session, at most
+static long long most_pages(const Kv8View& v, const Kv8Batch& q) {
+  return std::min((long long)q.bt_stride, v.max_context / kPage + 1ll);
+}
+
 // Places in the work are 32-bit: pages of all sessions and kv heads, or key
 // steps of all tiles. What a call can need at most, from its sizes.
 bool kv8_attention_fits(const Kv8View& v, const Kv8Batch& q, int group) {
-  const long long pages = std::min((long long)q.bt_stride, v.max_context / kPage + 1ll);
-  if ((long long)q.max_new * group <= kMaxCols) return q.B * pages * v.nkv < (1ll << 31);
-  return kv8_chunk_fits(v, q, group, pages);
+  const long long pages = most_pages(v, q);
+  return q.B * pages * v.nkv < (1ll << 31) && ((long long)q.max_new * group <= 8 || kv8_chunk_fits(v, q, group, pages));
 }
 
 cudaError_t kv8_attention(const Kv8View& v, const Kv8Batch& q, int d, int group, int sms, const uint16_t* qp,
@@ -744,7 +748,13 @@ cudaError_t kv8_attention(const Kv8View& v, const Kv8Batch& q, int d, int group,
   // the fewest n-tiles that hold every session's columns
   const long long cols = (long long)q.max_new * group;
   float* part = (float*)((char*)work + kCtas * (size_t)sms * sizeof(unsigned));
-  if (cols > kMaxCols)
+  // 9 to 16 columns of tiles that would be cut: the join of that many columns costs more
+  // than the tensor cores' kernel while the work is small (8 rows of 2 q heads a kv head
+  // behind 1000 tokens 27 and 19 us, 16 sessions of them 30 and 20; 8 sessions behind
+  // 2000 31 and 27, behind 8000 50 and 68)
+  const long long tiles = (long long)q.B * v.nkv, pages = most_pages(v, q);
+  const bool whole = tiles <= sms * kCtas && pages <= (2 * tiles >= sms * kCtas ? kWholePagesMany : kWholePages);
+  if (cols > kMaxCols || (cols > 8 && !whole && tiles * pages <= 128ll * sms))
     return kv8_chunk(v, q, d, group, sms, qp, q_stride, scale, out, out_stride, (unsigned*)work, part, s);
   const int nt = cols <= 8 ? 1 : 2;
   Args a{};

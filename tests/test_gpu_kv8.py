@@ -483,3 +483,13 @@ def test_sessions_that_share_rows_are_reported():
         assert r.status() == (qtts.QTTS_E_DEVICE, qtts.QTTS_DEV_BAD_SESSION)
         r.attend([60] * 3, [40] * 3)
         assert r.status() == (0, 0)
+
+
+@pytest.mark.parametrize("d,cap,lens,new", [(64, 40000, [1500], [8]), (128, 40000, [2100], [5]), (128, 14000, [900, 0, 1700], [8, 3, 6])])
+def test_nine_to_sixteen_columns_of_tables_for_long_sessions(d, cap, lens, new):
+    """Tiles cut over CTAs, 16 columns each: where the tables could hold long sessions."""
+    with Rig(len(lens), cap, nq=16, nkv=8, d=d) as r:
+        r.append([0] * len(lens), [a + b for a, b in zip(lens, new)])
+        q = r.rows(sum(new), 16)
+        a, b = r.attend(lens, new, q=q, pad=2), r.attend(lens, new, q=q, pad=2, check=False)
+        assert torch.equal(a, b) and r.status() == (0, 0)
