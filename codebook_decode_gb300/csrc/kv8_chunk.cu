@@ -164,9 +164,6 @@ __device__ __forceinline__ void load_if(float2& v, const void* p, bool yes) {
                : "+f"(v.x), "+f"(v.y)
                : "l"(p), "r"((uint32_t)yes));
 }
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
-}
 __device__ __forceinline__ void softmax_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
 }

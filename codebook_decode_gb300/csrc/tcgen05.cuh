@@ -16,6 +16,9 @@ __device__ __forceinline__ int word_at(int row, int word) { return row * 128 + (
 __device__ __forceinline__ uint64_t swizzled_desc(const void* p) {
   return (uint64_t)((smem_addr(p) >> 4) & 0x3FFFu) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;

@@ -367,11 +367,11 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 3 : NT <= 4 ? 2 : 1) w4_
 // 64 x 12288 x 2048 23 us against 29 of the kernel above, 48 x 30000 x 4096 64 against
 // 97: bound by the chain of a tile (product, sums, codes, barrier: 0.8 us), which two
 // CTAs an SM overlap.
-constexpr int kTcRows = 128, kTcTries = 1 << 17, NCOL = kW4MaxM;
+constexpr int kTcThreads = kW4Threads + 32, kTcRows = 128, kTcTries = 1 << 17, NCOL = kW4MaxM;
 constexpr int kTcSmem = 80 * 1024;
-__global__ void __launch_bounds__(kW4Threads, 2) w4_tc_kernel(const __grid_constant__ W4Args a) {
+__global__ void __launch_bounds__(kTcThreads, 2) w4_tc_kernel(const __grid_constant__ W4Args a) {
   extern __shared__ __align__(1024) uint8_t w4_tc_smem[];  // [2] weights, [4] activations; then the sums
-  __shared__ uint64_t bars[2];                             // the products of even, odd tiles have run
+  __shared__ uint64_t bars[2], full[2];                    // the products of even, odd tiles have run; their operands are there
   __shared__ uint32_t s_tmem;
   __shared__ int s_failed;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -387,6 +387,8 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_tc_kernel(const __grid_const
   if (tid == 0) {
     mbar_init(&bars[0], 1);
     mbar_init(&bars[1], 1);
+    mbar_init(&full[0], kW4Threads);
+    mbar_init(&full[1], kW4Threads);
     mbar_init_fence();
     s_failed = 0;
   }
@@ -396,6 +398,7 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_tc_kernel(const __grid_const
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   // this warp's codes, four tiles ahead; the scales of a thread's row, two tiles ahead of their use
+  const bool worker = warp < kW4Warps;  // the last warp issues the products
   const int rb = cta * 8 + warp, row = (warp & 3) * 32 + lane;
   const uint4* codes = a.codes + ((size_t)min(rb, a.RB - 1) * a.KT + t0) * 32 + lane;
   const int rbs = min(cta * 8 + row / 16, a.RB - 1);
@@ -408,7 +411,7 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_tc_kernel(const __grid_const
   };
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (i < n) w[i] = load_stream(codes + i * 32);
+    if (i < n && worker) w[i] = load_stream(codes + i * 32);
   load_scale(sc[0], 0);
   load_scale(sc[1], 1);
   tc_fence_before();
@@ -438,8 +441,6 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_tc_kernel(const __grid_const
       if (mbar_test_sleep(bar, parity, 10000)) return;
     *(volatile int*)&s_failed = 1;
   };
-  load_act(0);
-  load_act(1);
   constexpr int kCols = NCOL / 2;  // of a thread
   float acc[kCols];
 #pragma unroll
@@ -456,8 +457,28 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_tc_kernel(const __grid_const
       for (int c = 0; c < 16; ++c) acc[c0 + c] = fmaf(__uint_as_float(v[c]), s, acc[c0 + c]);
     }
   };
+  if (!worker) {
+    const bool leader = elect_one();
 #pragma unroll 1
-  for (int i0 = 0; i0 < n + 2; i0 += 4) {
+    for (int i = 0; i < n; ++i) {
+      wait(&full[i & 1], i >> 1 & 1);
+      tc_fence_after();
+      const uint64_t ad = swizzled_desc(wts + (i & 1) * (kTcRows * 128)), bd = swizzled_desc(act + (i & 3) * (NCOL * 128));
+      if (leader) {
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          tc_mma(tmem + accumulator(i, ks >> 1), ad + 2 * ks, bd + 2 * ks, tc_idesc_bf16(kTcRows, NCOL),
+                 fine ? ks & 1 : ks > 0 || (unit_log && (i & 1)));
+        tc_commit(&bars[i & 1]);
+      }
+      __syncwarp();
+    }
+  } else {
+    load_act(0);
+    load_act(1);
+  }
+#pragma unroll 1
+  for (int i0 = 0; i0 < n + 2 && worker; i0 += 4) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int i = i0 + u;
@@ -489,19 +510,7 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_tc_kernel(const __grid_const
       asm volatile("cp.async.wait_group 2;" ::: "memory");
       fence_async_shared();
       tc_fence_before();
-      __syncthreads();
-      if (warp == 0) {
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t ad = swizzled_desc(dst), bd = swizzled_desc(act + (i & 3) * (NCOL * 128));
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            tc_mma(tmem + accumulator(i, ks >> 1), ad + 2 * ks, bd + 2 * ks, tc_idesc_bf16(kTcRows, NCOL),
-                   fine ? ks & 1 : ks > 0 || (unit_log && (i & 1)));
-          tc_commit(&bars[i & 1]);
-        }
-        __syncwarp();
-      }
+      mbar_arrive(&full[i & 1]);
     }
   }
   tc_fence_before();
@@ -521,13 +530,14 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_tc_kernel(const __grid_const
 #pragma unroll
   for (int c = 0; c < kCols; ++c) {
     const int m = (warp >> 2) * kCols + c;
+    if (!worker) break;
     if (S == 1) put(m, row, acc[c] + poison);
     else part[m * kPitch + row] = acc[c] + poison;
   }
   if (S == 1) return;
   cluster.sync();
 #pragma unroll 1
-  for (int idx = rank * kW4Threads + tid; idx < kTcRows * a.M; idx += S * kW4Threads) {
+  for (int idx = rank * kTcThreads + tid; idx < kTcRows * a.M; idx += S * kTcThreads) {
     const int m = idx / kTcRows, r = idx % kTcRows;
     float v[kW4MaxSplit];
 #pragma unroll
@@ -577,7 +587,7 @@ cudaError_t w4_tc_launch(W4Args a, int sms, cudaStream_t s) {
   while ((1 << a.s_log) < kW4MaxSplit && ctas << a.s_log < sms && a.KT >= 8 << a.s_log) ++a.s_log;
   cudaLaunchConfig_t lc{};
   lc.gridDim = dim3(ctas << a.s_log);
-  lc.blockDim = dim3(kW4Threads);
+  lc.blockDim = dim3(kTcThreads);
   lc.dynamicSmemBytes = kTcSmem;
   lc.stream = s;
   cudaLaunchAttribute at[2];
