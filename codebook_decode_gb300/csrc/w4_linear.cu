@@ -364,9 +364,10 @@ __global__ void __launch_bounds__(kW4Threads, NT == 1 ? 3 : NT <= 4 ? 2 : 1) w4_
 // and shared memory is asked for so that an SM holds two CTAs at most: an allocation
 // never waits for a CTA that waits for this one.
 //
-// 64 x 12288 x 2048 23 us against 29 of the kernel above, 48 x 30000 x 4096 64 against
-// 97: bound by the chain of a tile (product, sums, codes, barrier: 0.8 us), which two
-// CTAs an SM overlap.
+// 64 x 12288 x 2048 19 us against 29 of the kernel above, 48 x 30000 x 4096 53 against
+// 97: bound by the chain of a tile (a product's sums, activations, codes), 0.6 us, which
+// two CTAs an SM overlap. A warp of its own issues the products (done by one of the
+// widening warps, behind a barrier: 23 and 64 us).
 constexpr int kTcThreads = kW4Threads + 32, kTcRows = 128, kTcTries = 1 << 17, NCOL = kW4MaxM;
 constexpr int kTcSmem = 80 * 1024;
 __global__ void __launch_bounds__(kTcThreads, 2) w4_tc_kernel(const __grid_constant__ W4Args a) {
@@ -420,15 +421,24 @@ __global__ void __launch_bounds__(kTcThreads, 2) w4_tc_kernel(const __grid_const
   const uint32_t tmem = s_tmem;
   grid_dependency_wait();  // activations
 
-  auto load_act = [&](int i) {  // tile i's activations, 16 bytes are 8 k; zeros beyond M and K
+  // tile i's activations, 16 bytes are 8 k; zeros beyond M and K
+  constexpr int kActs = NCOL * 8 / kW4Threads;
+  const int act_k = t0 * kW4K + (tid & 7) * 8;
+  const uint16_t* act_src[kActs];
+  uint32_t act_dst[kActs];
 #pragma unroll
-    for (int e = 0; e < NCOL * 8 / kW4Threads; ++e) {
-      const int idx = e * kW4Threads + tid, m = idx >> 3, word = idx & 7, k = (t0 + i) * kW4K + word * 8;
-      const bool in = i < n && m < a.M && k < a.K;
-      const uint16_t* src = in ? a.x + (int64_t)m * a.x_stride + k : a.x;
-      if (i < n)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(act + (i & 3) * (NCOL * 128) + word_at(m, word))),
-                     "l"(src), "r"(in ? 16 : 0)
+  for (int e = 0; e < kActs; ++e) {
+    const int m = (e * kW4Threads + tid) >> 3 & (NCOL - 1);
+    act_src[e] = m < a.M ? a.x + (int64_t)m * a.x_stride + act_k : nullptr;
+    act_dst[e] = smem_addr(act + word_at(m, tid & 7));
+  }
+  auto load_act = [&](int i) {
+    if (i < n) {
+      const bool in = act_k + i * kW4K < a.K;
+#pragma unroll
+      for (int e = 0; e < kActs; ++e)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(act_dst[e] + (i & 3) * (NCOL * 128)),
+                     "l"(in && act_src[e] ? act_src[e] + i * kW4K : a.x), "r"(in && act_src[e] ? 16 : 0)
                      : "memory");
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -773,7 +783,7 @@ int qtts_w4_linear(qtts_w4* w, int M, const uint16_t* x, int64_t x_stride, void*
   // activations and many blocks (12 x 2048 x 6144: 5.9 us with one, 8.1 with two;
   // 16 x 30000 x 4096 80 and 38). Clusters along k until the SMs have a CTA each
   // and while every warp keeps two k tiles. Over 32 rows the tcgen05 kernel where
-  // its clusters can fill three quarters of the SMs (64 x 4096 x 2048: 12.9 us
+  // its clusters can fill three quarters of the SMs (64 x 4096 x 2048: 11.4 us
   // against 15.5; 64 x 2048 x 6144: 26 against 12.7).
   const int blocks = M <= 8 ? 1 : M <= 16 ? 1 + (w->RB > 2 * w->G) : M <= 32 ? 1 : 2;  // row blocks of a warp
   auto ctas_of = [&](int rw_log) { return (w->RB + (blocks << rw_log) - 1) / (blocks << rw_log); };
