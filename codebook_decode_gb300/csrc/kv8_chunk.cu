@@ -122,10 +122,10 @@ struct Place {
 template <int D, bool TWO>
 struct ChunkSmem {
   alignas(1024) uint8_t q[TWO ? 2 : 1][kRows * D * 2];
-  uint8_t out[kRows * D * 2 * (TWO ? 2 : 1)];  // results on their way out
+  uint8_t out[kRows * D * 2 * (TWO ? 2 : 1)];  // results on their way out; before the first step the rows' query scales
   uint8_t k[2][kKeys * D * 2];
   uint8_t v[TWO ? 1 : 2][kKeys * D * 2];
-  float2 ml[2][kRows];  // each group's maximum and sum; before the first step the rows' query scales
+  float2 ml[2][kRows];  // each group's maximum and sum
   float4 sc[4][kPagesPerStep];  // a page's K scale, logarithm and reciprocal of its V scale
   // kfull, vfull: widened; kdone, vdone: read by the products; sdone: a group's
   // scores are there; pfull: its weights; pvdone: its second product has run;
@@ -570,6 +570,11 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
     uint32_t odd = 0;  // this group has had an odd number of steps
     bool ok = true;
     const Place& w = sm.at[kSoftmaxPlace];
+    // The rows' query scales stand in the results' place: that is next written behind
+    // two barriers of both groups. A place that one group writes when its steps are done
+    // would not do: a group without a step in this tile comes there while the other still
+    // reads its scales.
+    float* query_scale = (float*)sm.out;
 #pragma unroll 1
     while (left && ok) {
       const int cnt = min(left, w.steps - w.p);
@@ -607,7 +612,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
         mag = max(mag & 0xffffu, mag >> 16);
         const uint32_t ex = min(max(mag << 16 & 0x7f800000u, 1u << 23), 253u << 23);
         const float inv = __uint_as_float((254u << 23) - ex) * a.q_sign;
-        if (r < cols && at == 0) sm.ml[TWO ? r >> 7 : 1][r & 127].x = __uint_as_float(ex) * a.scale_log2;
+        if (r < cols && at == 0) query_scale[r] = __uint_as_float(ex) * a.scale_log2;
         uint8_t* dst = sm.q[TWO ? r >> 7 : 0] + (at & 4) * 2;
 #pragma unroll
         for (int k = 0; k < kQuads; ++k) {
@@ -634,7 +639,8 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
         }
       }
       softmax_sync();
-      const float cf = sm.ml[TWO ? x : 1][row].x;
+      const int tile_row = TWO ? 128 * x + row : row;
+      const float cf = tile_row < cols ? query_scale[tile_row] : 0.f;
       fence_async_shared();
       tc_fence_before();  // the last tile's accumulators have been read
       mbar_arrive(&sm.qfull);
