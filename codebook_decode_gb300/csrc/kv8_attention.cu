@@ -507,8 +507,8 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, kCtas) attention_kernel(con
               for (int k = 4; k < 32; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
               mx = fmaxf(mx, m[nt][e]);
               const float f = ex2(m[nt][e] - mx);
+              l[nt][e] = rebase(l[nt][e], m[nt][e], mx);
               m[nt][e] = mx;
-              l[nt][e] *= f;
 #pragma unroll
               for (int j = 0; j < VJ * 2; ++j) {
                 o[nt][j][e] *= f;
@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, kCtas) attention_kernel(con
         if (item++ % W != warp) continue;
         const bool in = run >> lane & 1;
         const float2 ml = in ? *(const float2*)(piece_col(lane, col) + D) : make_float2(kNone, 0.f);
-        const float mx = warp_max(ml.x), f = ex2(ml.x - mx), sum = warp_sum(ml.y * f);
+        const float mx = warp_max(ml.x), f = ex2(ml.x - mx), sum = warp_sum(rebase(ml.y, ml.x, mx));
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         for (uint32_t k = run; k; k &= k - 1) {
           const int i = __ffs(k) - 1;
@@ -645,8 +645,8 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, kCtas) attention_kernel(con
           const int i = i0 + lane * per;
           const float2 ml = i < pieces ? __ldcg((const float2*)(partial(i) + D)) : make_float2(kNone, 0.f);
           const float nm = fmaxf(mx, warp_max(ml.x)), f0 = ex2(mx - nm), f1 = ex2(ml.x - nm);
+          sum = rebase(sum, mx, nm) + warp_sum(rebase(ml.y, ml.x, nm));
           mx = nm;
-          sum = sum * f0 + warp_sum(ml.y * f1);
           v = make_float4(v.x * f0, v.y * f0, v.z * f0, v.w * f0);
           for (int k = 0; k < 32 && i0 + k * per < pieces; k += 8) {
             float4 y[8];  // eight loads in flight
@@ -677,7 +677,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, kCtas) attention_kernel(con
           for (int k = 0; k < per; ++k) {
             const float* src = parts + (warp + k) * kCol;
             const float f = ex2(src[D] - mx);
-            sum += src[D + 1] * f;
+            sum += rebase(src[D + 1], src[D], mx);
             if (lane < D / 4) axpy(v, *(const float4*)(src + 4 * lane), f);
           }
           if (lane < D / 4) write(pc.row, pc.h, warp / per, 4 * lane, v, sum);

@@ -37,6 +37,13 @@ __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
   return *(const uint32_t*)&h;
 }
 
+// A sum of weights relative to 2^from, relative to 2^to. In two halves: the maxima follow
+// weight times V scale, so a first block of zeros (held at 2^-100) leaves a sum of up to
+// 2^118 behind, which counts beside large values though the whole factor is below fp32's range.
+__device__ __forceinline__ float rebase(float sum, float from, float to) {
+  const float half = ex2(0.5f * (from - to));
+  return sum * half * half;
+}
 __device__ __forceinline__ void axpy(float4& v, float4 x, float f) {
   v = make_float4(fmaf(x.x, f, v.x), fmaf(x.y, f, v.y), fmaf(x.z, f, v.z), fmaf(x.w, f, v.w));
 }

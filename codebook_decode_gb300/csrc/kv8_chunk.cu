@@ -126,7 +126,9 @@ struct ChunkSmem {
   uint8_t k[2][kKeys * D * 2];
   uint8_t v[TWO ? 1 : 2][kKeys * D * 2];
   float2 ml[2][kRows];  // each group's maximum and sum
-  float4 sc[4][kPagesPerStep];  // a page's K scale, logarithm and reciprocal of its V scale
+  // a page's K scale, logarithm of its V scale (for the maximum), and the V scale that its
+  // weights are multiplied with: reciprocal and logarithm
+  float4 sc[4][kPagesPerStep];
   // kfull, vfull: widened; kdone, vdone: read by the products; sdone: a group's
   // scores are there; pfull: its weights; pvdone: its second product has run;
   // qfull: the tile's queries; drained: after a failure, all products issued
@@ -178,6 +180,12 @@ __device__ __forceinline__ void set_regs_down() {
 __device__ __forceinline__ uint32_t bf2_bits(float a, float b) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
   return *(const uint32_t*)&p;
+}
+// largest finite halves for what is above them: weights of blocks of zeros
+__device__ __forceinline__ uint32_t half2_finite(float a, float b) {
+  uint32_t d;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+  return d;
 }
 __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if one is
   float d;
@@ -419,8 +427,10 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
           if (!ok) break;
           if (lane < 2) {
             const float2 v = lane ? sc[1] : sc[0];
-            const float sv = v.y != v.y ? v.y : fmaxf(v.y, kKv8MinScale);
-            sm.sc[j & 3][wp + lane] = make_float4(v.x, lg2(sv), 1.f / sv, 0.f);
+            // A block of zeros moves no maximum, and its weights, multiplied with nothing but
+            // zeros, are only summed: as they are, since 2^-100 of them may be below fp32's range.
+            const float sv = v.y != v.y ? v.y : fmaxf(v.y, kKv8MinScale), lv = lg2(sv);
+            sm.sc[j & 3][wp + lane] = make_float4(v.x, lv, v.y == 0.f ? 1.f : 1.f / sv, v.y == 0.f ? 0.f : lv);
           }
 #pragma unroll
           for (int i = 0; i < 2; ++i)
@@ -707,8 +717,10 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
           const bool grow = mx > m + kSlack;
           if (__builtin_expect(__any_sync(0xffffffffu, grow), 0)) {
             const float f = grow ? ex2(m - mx) : 1.f;
-            if (grow) m = mx;
-            l *= f;
+            if (grow) {
+              l = rebase(l, m, mx);
+              m = mx;
+            }
             if (any) {
 #pragma unroll 1
               for (int c = 0; c < D / 16; ++c) {
@@ -726,7 +738,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
           // 8 columns from 8 page on.
           auto weights = [&](uint32_t (&v)[16], int page) {
             const float4 f = factors(page);
-            const uint64_t mul = pack2(f.x, f.x), off = pack2(f.y - m, f.y - m);
+            const uint64_t mul = pack2(f.x, f.x), off = pack2(f.w - m, f.w - m);
             uint64_t sum = 0;
             uint32_t h[8];
 #pragma unroll
@@ -734,7 +746,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
               const float2 y = unpack2(fma2(pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), mul, off));
               const float p0 = ex2(y.x), p1 = ex2(y.y);  // weight times V scale
               sum = add2(sum, pack2(p0, p1));
-              h[e] = half2_bits(p0, p1);
+              h[e] = half2_finite(p0, p1);
             }
             const float2 t = unpack2(sum);
             l = fmaf(t.x + t.y, f.z, l);
@@ -778,7 +790,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
         const float mj = fmaxf(mlA.x, mlB.x);
         fA = ex2(mlA.x - mj);
         fB = ex2(mlB.x - mj);
-        ml = make_float2(mj, mlA.y * fA + mlB.y * fB);
+        ml = make_float2(mj, rebase(mlA.y, mlA.x, mj) + rebase(mlB.y, mlB.x, mj));
       }
       const bool hasA = TWO ? x == 0 : cnt > 1 || ((j - 1) & 1) == 0, hasB = TWO ? x == 1 : cnt > 1 || ((j - 1) & 1) == 1;
       const bool starts = w.p == 0, ends = w.p + cnt == w.steps;
@@ -861,7 +873,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
             for (int i = 0; i < pieces; ++i) {
               const float2 y = sums(i);
               const float f = ex2(y.x - mj);
-              sum += y.y * f;
+              sum += rebase(y.y, y.x, mj);
 #pragma unroll
               for (int e = 0; e < 4; ++e) axpy(v[e], __ldcg(of(i) + (4 * at + e) * kTile + r), f);
             }

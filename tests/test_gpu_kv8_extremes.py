@@ -1,0 +1,28 @@
+"""Attention over the 8-bit cache where weights or values leave the usual range."""
+import kv8_exact as ex
+import numpy as np
+import pytest
+from kv8_ref import bf16
+from test_gpu_kv8_exact import Held
+
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nq,nkv,new", [(2, 1, 1), (2, 1, 40), (64, 8, 1100)])
+@pytest.mark.parametrize("big", [0, 30, 60])
+def test_blocks_of_zeros_keep_their_weights(d, nq, nkv, new, big):
+    """V blocks of zeros (four pages of every eight) beside blocks of 127 * 2^big: the zeros' tokens count in the mean."""
+    n = 1200 + new
+    page = np.arange(n) // 16
+    k = np.full((n, nkv, d), 1.0)
+    v = np.zeros((n, nkv, d))
+    v[page % 8 >= 4] = 127 * 2.0 ** big
+    q = bf16(np.ones((new, nq, d)))[0]
+    lens = n - new
+    with Held([n], nq, nkv, d, [k], [v]) as c:
+        got, _ = c.attend(q, [lens], [new], 0.0)
+    seen = lens + np.arange(new)
+    want = (np.cumsum(v[:, 0, 0])[seen] / (seen + 1))[:, None, None]
+    assert np.all(np.abs(got - want) <= ex.mean_bound(want))
