@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, kCtas) attention_kernel(con
           for (int e = 0; e < 4; ++e) v[e] = p[e] * sc.y;
           if (page >= first_masked) {  // what a column does not see gives nothing, whatever its scale
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = p[e] > 0.f || p[e] != p[e] ? v[e] : 0.f;
+            for (int e = 0; e < 4; ++e) v[e] = page * kPage + g + (e >> 1) * 8 > see[nt][e & 1] ? 0.f : v[e];
           }
           pf[nt][0] = transpose8(half2_bits(v[0], v[1]));
           pf[nt][1] = transpose8(half2_bits(v[2], v[3]));
