@@ -391,8 +391,12 @@ Kv8View view(const qtts_kv8* c, int layer) {
   return {c->codes + blocks * 32 * f.head_dim, c->scales + blocks * 2, c->rope_cos, c->rope_sin, f.n_kv_heads,
           f.pool_pages, f.max_context, c->dev_err};
 }
-// pages that max_new rows can touch, wherever they start
-int touched_pages(int max_new) { return (max_new + 2 * kPage - 2) / kPage; }
+// Pages that a session's rows can touch, wherever they start. max_new and n_rows are
+// bounds that a caller may set as high as it likes; a session ends at max_context.
+int touched_pages(int max_new, int n_rows, int max_context) {
+  return (std::min({max_new, n_rows, max_context}) + 2 * kPage - 2) / kPage;
+}
+static_assert((kKv8MaxContext + 2 * kPage) / kPage * (long long)kKv8MaxBatch <= 0x7fffffff, "CTAs of a grid");
 
 template <typename... P, typename... A>
 cudaError_t launch(void (*kern)(P...), dim3 grid, int threads, cudaStream_t s, A... args) {
@@ -526,8 +530,7 @@ int qtts_kv8_append(qtts_kv8* c, int layer, int B, int n_rows, int max_new, cons
   if (rc) return QTTS_OK;
   DeviceGuard g(c->device);
   if (!g.ok) return fail(c, QTTS_E_CUDA, "cudaSetDevice failed");
-  const int touched = touched_pages(std::min(max_new, n_rows));
-  if ((long long)B * touched > 0x7fffffffll) return fail(c, QTTS_E_INVALID, "qtts_kv8_append: too many rows");
+  const int touched = touched_pages(max_new, n_rows, f.max_context);
   const int warps = std::min(2 * f.n_kv_heads, kMaxWarps);
   const dim3 grid(B * touched, (2 * f.n_kv_heads + warps - 1) / warps);
   const cudaError_t e = launch(f.head_dim == 64 ? append_kernel<64> : append_kernel<128>, grid, warps * 32,
@@ -550,8 +553,7 @@ int qtts_kv8_read(qtts_kv8* c, int layer, int B, int n_rows, int max_new, const 
   if (rc) return QTTS_OK;
   DeviceGuard g(c->device);
   if (!g.ok) return fail(c, QTTS_E_CUDA, "cudaSetDevice failed");
-  const int touched = touched_pages(std::min(max_new, n_rows));
-  if ((long long)B * touched > 0x7fffffffll) return fail(c, QTTS_E_INVALID, "qtts_kv8_read: too many rows");
+  const int touched = touched_pages(max_new, n_rows, f.max_context);
   const int warps = std::min(2 * f.n_kv_heads, kMaxWarps);
   const dim3 grid(B * touched, (2 * f.n_kv_heads + warps - 1) / warps);
   const cudaError_t e = launch(f.head_dim == 64 ? read_kernel<64> : read_kernel<128>, grid, warps * 32,
