@@ -740,7 +740,7 @@ static long long most_pages(const Kv8View& v, const Kv8Batch& q) {
 // steps of all tiles. What a call can need at most, from its sizes.
 bool kv8_attention_fits(const Kv8View& v, const Kv8Batch& q, int group) {
   const long long pages = most_pages(v, q);
-  return q.B * pages * v.nkv < (1ll << 31) && ((long long)q.max_new * group <= 8 || kv8_chunk_fits(v, q, group, pages));
+  return q.B * pages * v.nkv < (1ll << 31) && ((long long)q.max_new * group <= kMaxCols || kv8_chunk_fits(v, q, group, pages));
 }
 
 cudaError_t kv8_attention(const Kv8View& v, const Kv8Batch& q, int d, int group, int sms, const uint16_t* qp,
@@ -754,7 +754,7 @@ cudaError_t kv8_attention(const Kv8View& v, const Kv8Batch& q, int d, int group,
   // 2000 31 and 27, behind 8000 50 and 68)
   const long long tiles = (long long)q.B * v.nkv, pages = most_pages(v, q);
   const bool whole = tiles <= sms * kCtas && pages <= (2 * tiles >= sms * kCtas ? kWholePagesMany : kWholePages);
-  if (cols > kMaxCols || (cols > 8 && !whole && tiles * pages <= 128ll * sms))
+  if (cols > kMaxCols || (cols > 8 && !whole && tiles * pages <= 128ll * sms && kv8_chunk_fits(v, q, group, pages)))
     return kv8_chunk(v, q, d, group, sms, qp, q_stride, scale, out, out_stride, (unsigned*)work, part, s);
   const int nt = cols <= 8 ? 1 : 2;
   Args a{};

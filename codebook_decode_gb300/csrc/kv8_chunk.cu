@@ -935,15 +935,20 @@ cudaError_t kv8_chunk_setup(int d) {
 
 size_t kv8_chunk_workspace(int d, int sms) { return 2 * (size_t)sms * 2 * kRows * (d + 4) * sizeof(float); }
 
+// Rows that the call's sessions can have: n_rows and max_new are bounds of any size.
+static long long most_rows(const Kv8View& v, const Kv8Batch& q) {
+  return std::min((long long)q.n_rows, (long long)q.B * std::min(q.max_new, v.max_context));
+}
+
 bool kv8_chunk_fits(const Kv8View& v, const Kv8Batch& q, int group, long long pages) {
-  const long long tiles = q.n_rows / (kRows / group) + q.B, steps = pages * kPage / kKeys + 2;
+  const long long tiles = most_rows(v, q) / (kRows / group) + q.B, steps = pages * kPage / kKeys + 2;
   return tiles * v.nkv < ((1ll << 31) - 4096) / steps;  // 4096: rounding up to shares
 }
 
 cudaError_t kv8_chunk(const Kv8View& v, const Kv8Batch& q, int d, int group, int sms, const uint16_t* qp,
                       int64_t q_stride, float scale, uint16_t* out, int64_t out_stride, unsigned* arrived, float* part,
                       cudaStream_t s) {
-  const bool two = (long long)q.n_rows * group * v.nkv >= 2ll * sms * 2 * kRows;
+  const bool two = most_rows(v, q) * group * v.nkv >= 2ll * sms * 2 * kRows;
   ChunkArgs a{v, q, group, (two ? 2 : 1) * kRows / group, (65536 + group - 1) / group, qp, q_stride, std::fabs(scale) * kLog2e,
               scale < 0.f ? -1.f : 1.f, out, out_stride, part, arrived};
   if (d == 64) return two ? launch_chunk<64, true>(a, sms, s) : launch_chunk<64, false>(a, sms, s);

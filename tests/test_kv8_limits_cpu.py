@@ -26,3 +26,10 @@ def said(tmp_path_factory):
 def test_pages_that_a_sessions_rows_can_touch(said, name, pages):
     """n rows touch at most 1 + ceil((n - 1) / 16) pages."""
     assert said[name] == pages
+
+
+@pytest.mark.parametrize("name,fits", [
+    ("fits_8_columns", 1), ("fits_16_columns", 1), ("fits_16_columns_one_session", 1), ("fits_no_bounds", 1),
+    ("fits_largest_prompt", 1), ("fits_too_many_pages", 0), ("fits_too_many_rows", 0)])
+def test_attention_is_refused_only_for_what_its_sessions_can_have(said, name, fits):
+    assert said[name] == fits
