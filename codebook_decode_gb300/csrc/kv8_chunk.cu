@@ -131,7 +131,7 @@ struct ChunkSmem {
   float4 sc[4][kPagesPerStep];
   // kfull, vfull: widened; kdone, vdone: read by the products; sdone: a group's
   // scores are there; pfull: its weights; pvdone: its second product has run;
-  // qfull: the tile's queries; drained: after a failure, all products issued
+  // qfull: the tile's queries; drained: all products have run
   uint64_t kfull[2], vfull[2], kdone[2], vdone[2], sdone[2], pfull[2], pvdone[2], qfull, drained;
   Place at[kPlaces];  // of the widening warps, the issuing warp and the softmax groups
   uint32_t tmem;
@@ -562,12 +562,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) chunk_kernel(const __grid_consta
         if (leader && left) sm.at[kIssuePlace].advance(a, cnt);
         __syncwarp();
       }
-      if (!ok) {  // what was issued has to end before the tensor memory is given back
-        if (leader) tc_commit(&sm.drained);
-#pragma unroll 1
-        for (int tries = 0; tries < kChunkTries; ++tries)
-          if (mbar_test_sleep(&sm.drained, 0, 10000)) break;
-      }
+      drain_products(&sm.drained, kChunkTries);
     }
     __syncwarp();
   } else {

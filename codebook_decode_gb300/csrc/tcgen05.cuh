@@ -25,6 +25,17 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
   return p != 0;
 }
+// Waits, with a limit, until every product that this warp's elected lane has issued has
+// run: before the tensor memory is given back, whichever other wait ran out its own limit.
+// `bar`: initialised for one arrival, of no other use; whole warp.
+__device__ __forceinline__ void drain_products(uint64_t* bar, int tries) {
+  if (elect_one()) tc_commit(bar);
+  __syncwarp();
+#pragma unroll 1
+  for (int i = 0; i < tries; ++i)
+    if (mbar_test_sleep(bar, 0, 10000)) break;
+  __syncwarp();
+}
 __device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t at) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"

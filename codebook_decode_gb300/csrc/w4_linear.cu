@@ -373,6 +373,7 @@ constexpr int kTcSmem = 80 * 1024;
 __global__ void __launch_bounds__(kTcThreads, 2) w4_tc_kernel(const __grid_constant__ W4Args a) {
   extern __shared__ __align__(1024) uint8_t w4_tc_smem[];  // [2] weights, [4] activations; then the sums
   __shared__ uint64_t bars[2], full[2];                    // the products of even, odd tiles have run; their operands are there
+  __shared__ uint64_t drained;                             // all products have run
   __shared__ uint32_t s_tmem;
   __shared__ int s_failed;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -390,6 +391,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) w4_tc_kernel(const __grid_const
     mbar_init(&bars[1], 1);
     mbar_init(&full[0], kW4Threads);
     mbar_init(&full[1], kW4Threads);
+    mbar_init(&drained, 1);
     mbar_init_fence();
     s_failed = 0;
   }
@@ -443,7 +445,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) w4_tc_kernel(const __grid_const
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  // bounded; a product that does not end gives NaN
+  // Bounded; a product that does not end gives NaN. After a failure the loops go on, with
+  // waits that give up at once (leaving the loops by a vote cost 3 %).
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (mbar_test(bar, parity)) return;
 #pragma unroll 1
@@ -483,6 +486,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) w4_tc_kernel(const __grid_const
       }
       __syncwarp();
     }
+    drain_products(&drained, kTcTries);
   } else {
     load_act(0);
     load_act(1);
