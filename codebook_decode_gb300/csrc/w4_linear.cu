@@ -787,8 +787,13 @@ int qtts_w4_linear(qtts_w4* w, int M, const uint16_t* x, int64_t x_stride, void*
   // activations and many blocks (12 x 2048 x 6144: 5.9 us with one, 8.1 with two;
   // 16 x 30000 x 4096 80 and 38). Clusters along k until the SMs have a CTA each
   // and while every warp keeps two k tiles. Over 32 rows the tcgen05 kernel where
-  // its clusters can fill three quarters of the SMs (64 x 4096 x 2048: 11.4 us
-  // against 15.5; 64 x 2048 x 6144: 26 against 12.7).
+  // four CTAs for each 128 weight rows are three quarters of the SMs or more (from 3585
+  // rows on; 64 x 4096 x 2048: 11.4 us against 15.5; 64 x 2048 x 6144: 26 against 12.7),
+  // split as far as K allows: with few k tiles its CTAs are fewer but short (64 x 6144 x
+  // 256: 5.4 us against 5.6, 33 rows 5.3 against 4.1; 64 x 12288 x 256 6.1 against 10.8). With 8 to 15 k tiles it
+  // is slower than the other kernel where that one's CTAs, one an SM and then not split,
+  // are all there at once (64 x 6144 x 512: 9.1 us against 6.6, 33 x 9728 x 768 7.9
+  // against 6.3; 64 x 6144 x 1024, two waves: 8.6 against 15.7).
   const int blocks = M <= 8 ? 1 : M <= 16 ? 1 + (w->RB > 2 * w->G) : M <= 32 ? 1 : 2;  // row blocks of a warp
   auto ctas_of = [&](int rw_log) { return (w->RB + (blocks << rw_log) - 1) / (blocks << rw_log); };
   if (M <= 8) {
@@ -803,7 +808,8 @@ int qtts_w4_linear(qtts_w4* w, int M, const uint16_t* x, int64_t x_stride, void*
   if (M <= 8) e = w4_launch<1, 1>(a, s);
   else if (M <= 16) e = blocks == 1 ? w4_launch<2, 1>(a, s) : w4_launch<2, 2>(a, s);
   else if (M <= 32) e = w4_launch<4, 1>(a, s);
-  else if (4 * ((w->RB + 7) / 8 * kW4MaxSplit) >= 3 * w->G) e = w4_tc_launch(a, w->G, s);
+  else if (4 * ((w->RB + 7) / 8 * kW4MaxSplit) >= 3 * w->G && !(w->KT >= 8 && w->KT < 16 && ctas_of(a.rw_log) <= w->G))
+    e = w4_tc_launch(a, w->G, s);
   else e = w4_launch<8, 2>(a, s);
   if (e != cudaSuccess) {
     cudaGetLastError();  // reported here, not by the caller's next CUDA call
