@@ -347,10 +347,10 @@ int fail(qtts_kv8* c, int code, const char* fmt, ...) {
   return code;
 }
 
-// A failed launch is reported here, not by the caller's next CUDA call.
-int launch_fault(qtts_kv8* c, const char* who, cudaError_t e) {
+// A failed runtime call is reported here, not by a later call's check of the last error.
+int cuda_fault(qtts_kv8* c, const char* who, cudaError_t e) {
   cudaGetLastError();
-  return fail(c, QTTS_E_CUDA, "%s: %s", who, cudaGetErrorString(e));
+  return fail(c, e == cudaErrorMemoryAllocation ? QTTS_E_OOM : QTTS_E_CUDA, "%s: %s", who, cudaGetErrorString(e));
 }
 
 const char* config_fault(const qtts_kv8_config& c) {
@@ -423,16 +423,15 @@ int qtts_kv8_create(const qtts_kv8_config* cfg, int device, qtts_kv8** out) {
   *out = nullptr;
   if (const char* why = config_fault(*cfg)) return fail(nullptr, QTTS_E_INVALID, "bad config: %s", why);
   int ndev = 0;
-  if (cudaGetDeviceCount(&ndev) != cudaSuccess || device < 0 || device >= ndev)
-    return fail(nullptr, QTTS_E_CUDA, "no CUDA device %d", device);
+  if (cudaGetDeviceCount(&ndev) != cudaSuccess) cudaGetLastError();
+  if (device < 0 || device >= ndev) return fail(nullptr, QTTS_E_CUDA, "no CUDA device %d", device);
   DeviceGuard g(device);
   if (!g.ok) return fail(nullptr, QTTS_E_CUDA, "cudaSetDevice(%d) failed", device);
   qtts_kv8* c = new (std::nothrow) qtts_kv8();
   if (!c) return fail(nullptr, QTTS_E_OOM, "out of host memory");
-  auto bail = [&](int code, const char* what, cudaError_t e) {
-    fail(nullptr, code, "%s: %s", what, cudaGetErrorString(e));
+  auto bail = [&](const char* what, cudaError_t e) {
     qtts_kv8_destroy(c);
-    return code;
+    return cuda_fault(nullptr, what, e);
   };
   c->cfg = *cfg;
   c->device = device;
@@ -441,12 +440,12 @@ int qtts_kv8_create(const qtts_kv8_config* cfg, int device, qtts_kv8** out) {
     c->seen_now.assign(cfg->pool_pages, 0);
     c->free_ids.resize(cfg->pool_pages);
   } catch (const std::bad_alloc&) {
-    return bail(QTTS_E_OOM, "page list", cudaErrorMemoryAllocation);
+    return bail("page list", cudaErrorMemoryAllocation);
   }
   for (int i = 0; i < cfg->pool_pages; ++i) c->free_ids[i] = cfg->pool_pages - 1 - i;  // handed out 0, 1, 2, ...
   cudaError_t e = cudaDeviceGetAttribute(&c->G, cudaDevAttrMultiProcessorCount, device);
   if (e == cudaSuccess) e = kv8_attention_setup(cfg->head_dim);
-  if (e != cudaSuccess) return bail(QTTS_E_CUDA, "kernel setup", e);
+  if (e != cudaSuccess) return bail("kernel setup", e);
   const size_t blocks = (size_t)cfg->n_layers * cfg->pool_pages * cfg->n_kv_heads;
   const size_t half = cfg->head_dim / 2, table = (size_t)cfg->max_context * half * sizeof(float);
   e = cudaMalloc((void**)&c->codes, blocks * 32 * cfg->head_dim);
@@ -454,10 +453,7 @@ int qtts_kv8_create(const qtts_kv8_config* cfg, int device, qtts_kv8** out) {
   if (e == cudaSuccess) e = cudaMalloc((void**)&c->dev_err, sizeof(int));
   if (e == cudaSuccess && cfg->rope_theta > 0.f) e = cudaMalloc((void**)&c->rope_cos, table);
   if (e == cudaSuccess && cfg->rope_theta > 0.f) e = cudaMalloc((void**)&c->rope_sin, table);
-  if (e != cudaSuccess) {
-    cudaGetLastError();  // reported here, not by a later call
-    return bail(QTTS_E_OOM, "device allocation", e);
-  }
+  if (e != cudaSuccess) return bail("device allocation", e);
   // pages start as zero scales: a page that was never appended to reads as 0
   e = cudaMemset(c->scales, 0, blocks * 2 * sizeof(float));
   if (e == cudaSuccess) e = cudaMemset(c->codes, 128, blocks * 32 * cfg->head_dim);
@@ -466,7 +462,7 @@ int qtts_kv8_create(const qtts_kv8_config* cfg, int device, qtts_kv8** out) {
     e = launch(rope_table_kernel, dim3(std::min(cfg->max_context, 4096)), (int)half, nullptr, c->rope_cos, c->rope_sin,
                cfg->max_context, (int)half, (double)cfg->rope_theta);
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
-  if (e != cudaSuccess) return bail(QTTS_E_CUDA, "cache setup", e);
+  if (e != cudaSuccess) return bail("cache setup", e);
   *out = c;
   return QTTS_OK;
 }
@@ -476,7 +472,7 @@ void qtts_kv8_destroy(qtts_kv8* c) {
   {
     DeviceGuard g(c->device);
     for (void* p : {(void*)c->codes, (void*)c->scales, (void*)c->rope_cos, (void*)c->rope_sin, (void*)c->dev_err})
-      if (p) cudaFree(p);
+      if (p && cudaFree(p) != cudaSuccess) cudaGetLastError();
   }
   delete c;
 }
@@ -535,7 +531,7 @@ int qtts_kv8_append(qtts_kv8* c, int layer, int B, int n_rows, int max_new, cons
   const dim3 grid(B * touched, (2 * f.n_kv_heads + warps - 1) / warps);
   const cudaError_t e = launch(f.head_dim == 64 ? append_kernel<64> : append_kernel<128>, grid, warps * 32,
                                (cudaStream_t)stream, view(c, layer), q, touched, k, k_stride, v, v_stride);
-  if (e != cudaSuccess) return launch_fault(c, "qtts_kv8_append", e);
+  if (e != cudaSuccess) return cuda_fault(c, "qtts_kv8_append", e);
   return QTTS_OK;
 }
 
@@ -558,7 +554,7 @@ int qtts_kv8_read(qtts_kv8* c, int layer, int B, int n_rows, int max_new, const 
   const dim3 grid(B * touched, (2 * f.n_kv_heads + warps - 1) / warps);
   const cudaError_t e = launch(f.head_dim == 64 ? read_kernel<64> : read_kernel<128>, grid, warps * 32,
                                (cudaStream_t)stream, view(c, layer), q, touched, k_out, v_out);
-  if (e != cudaSuccess) return launch_fault(c, "qtts_kv8_read", e);
+  if (e != cudaSuccess) return cuda_fault(c, "qtts_kv8_read", e);
   return QTTS_OK;
 }
 
@@ -585,7 +581,7 @@ int qtts_kv8_attention(qtts_kv8* c, int layer, int B, int n_rows, int max_new, c
   if (!g.ok) return fail(c, QTTS_E_CUDA, "cudaSetDevice failed");
   const cudaError_t e = kv8_attention(view(c, layer), qb, f.head_dim, f.n_q_heads / f.n_kv_heads, c->G, q, q_stride,
                                       scale, out, out_stride, workspace, (cudaStream_t)stream);
-  if (e != cudaSuccess) return launch_fault(c, "qtts_kv8_attention", e);
+  if (e != cudaSuccess) return cuda_fault(c, "qtts_kv8_attention", e);
   return QTTS_OK;
 }
 
@@ -598,7 +594,7 @@ int qtts_kv8_status(qtts_kv8* c, int* device_err) {
   cudaError_t e = cudaDeviceSynchronize();
   if (e == cudaSuccess) e = cudaMemcpy(&v, c->dev_err, sizeof(int), cudaMemcpyDeviceToHost);
   if (e == cudaSuccess && v) e = cudaMemset(c->dev_err, 0, sizeof(int));
-  if (e != cudaSuccess) return fail(c, QTTS_E_CUDA, "qtts_kv8_status: %s", cudaGetErrorString(e));
+  if (e != cudaSuccess) return cuda_fault(c, "qtts_kv8_status", e);
   if (device_err) *device_err = v;
   if (v == QTTS_DEV_TIMEOUT) return fail(c, QTTS_E_TIMEOUT, "a device-side wait ran out its limit");
   if (v) return fail(c, QTTS_E_DEVICE, "device-side check failed: %d", v);

@@ -270,6 +270,7 @@ struct DeviceGuard {
   explicit DeviceGuard(int d) : dev(d) {
     if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
     ok = prev == d || cudaSetDevice(d) == cudaSuccess;
+    if (!ok || prev < 0) cudaGetLastError();  // reported by the caller, not by a later check of the last error
   }
   ~DeviceGuard() {
     if (prev >= 0 && prev != dev) cudaSetDevice(prev);

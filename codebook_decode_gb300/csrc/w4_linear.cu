@@ -623,11 +623,17 @@ int fail(qtts_w4* w, int code, const char* fmt, ...) {
   return code;
 }
 
+// A failed runtime call is reported here, not by a later call's check of the last error.
+int cuda_fault(qtts_w4* w, const char* who, cudaError_t e) {
+  cudaGetLastError();
+  return fail(w, e == cudaErrorMemoryAllocation ? QTTS_E_OOM : QTTS_E_CUDA, "%s: %s", who, cudaGetErrorString(e));
+}
+
 struct DeviceBuf {
   void* p = nullptr;
   cudaError_t alloc(size_t n) { return cudaMalloc(&p, n); }
   ~DeviceBuf() {
-    if (p) cudaFree(p);
+    if (p && cudaFree(p) != cudaSuccess) cudaGetLastError();
   }
 };
 
@@ -648,8 +654,8 @@ int qtts_w4_create(int N, int K, int group, int device, qtts_w4** out) {
   if (K % group) return fail(nullptr, QTTS_E_INVALID, "K must be a multiple of the group");
   if (N > (1 << 24) || K > (1 << 20)) return fail(nullptr, QTTS_E_INVALID, "N must be at most 2^24 and K at most 2^20");
   int ndev = 0;
-  if (cudaGetDeviceCount(&ndev) != cudaSuccess || device < 0 || device >= ndev)
-    return fail(nullptr, QTTS_E_CUDA, "no CUDA device %d", device);
+  if (cudaGetDeviceCount(&ndev) != cudaSuccess) cudaGetLastError();
+  if (device < 0 || device >= ndev) return fail(nullptr, QTTS_E_CUDA, "no CUDA device %d", device);
   DeviceGuard g(device);
   if (!g.ok) return fail(nullptr, QTTS_E_CUDA, "cudaSetDevice(%d) failed", device);
   qtts_w4* w = new (std::nothrow) qtts_w4();
@@ -667,10 +673,8 @@ int qtts_w4_create(int N, int K, int group, int device, qtts_w4** out) {
   if (e == cudaSuccess) e = cudaMalloc((void**)&w->scales, ns * sizeof(uint16_t));
   if (e == cudaSuccess) e = cudaMemset(w->scales, 0, ns * sizeof(uint16_t));
   if (e != cudaSuccess) {
-    cudaGetLastError();
-    fail(nullptr, QTTS_E_OOM, "device allocation: %s", cudaGetErrorString(e));
     qtts_w4_destroy(w);
-    return QTTS_E_OOM;
+    return cuda_fault(nullptr, "qtts_w4_create", e);
   }
   *out = w;
   return QTTS_OK;
@@ -680,8 +684,8 @@ void qtts_w4_destroy(qtts_w4* w) {
   if (!w) return;
   {
     DeviceGuard g(w->device);
-    if (w->codes) cudaFree(w->codes);
-    if (w->scales) cudaFree(w->scales);
+    for (void* p : {(void*)w->codes, (void*)w->scales})
+      if (p && cudaFree(p) != cudaSuccess) cudaGetLastError();
   }
   delete w;
 }
@@ -695,10 +699,7 @@ static int w4_fill(qtts_w4* w, const void* src, size_t src_bytes, const void* sc
   if (e == cudaSuccess && !scales) e = q.alloc(nk);
   if (e == cudaSuccess) e = s.alloc(ns * sizeof(uint16_t));
   if (e == cudaSuccess) e = bad.alloc(sizeof(int));
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return fail(w, QTTS_E_OOM, "%s: %s", who, cudaGetErrorString(e));
-  }
+  if (e != cudaSuccess) return cuda_fault(w, who, e);
   const int grid = 8 * w->G;
   int flag = 0;
   w->loaded = false;
@@ -718,7 +719,7 @@ static int w4_fill(qtts_w4* w, const void* src, size_t src_bytes, const void* sc
   }
   if (e == cudaSuccess) e = cudaMemcpy(&flag, bad.p, sizeof(int), cudaMemcpyDeviceToHost);
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
-  if (e != cudaSuccess) return fail(w, QTTS_E_CUDA, "%s: %s", who, cudaGetErrorString(e));
+  if (e != cudaSuccess) return cuda_fault(w, who, e);
   if (flag) return fail(w, QTTS_E_INVALID, "%s: a code outside -8..7", who);
   w->loaded = true;
   return QTTS_OK;
@@ -746,15 +747,12 @@ int qtts_w4_export(qtts_w4* w, int8_t* codes_host, uint16_t* scales_host) {
   DeviceBuf q, s;
   cudaError_t e = q.alloc(nk);
   if (e == cudaSuccess) e = s.alloc(ns * sizeof(uint16_t));
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return fail(w, QTTS_E_OOM, "qtts_w4_export: %s", cudaGetErrorString(e));
-  }
+  if (e != cudaSuccess) return cuda_fault(w, "qtts_w4_export", e);
   w4_unpack_kernel<<<8 * w->G, 256>>>(w->codes, w->scales, w->N, w->K, w->group, w->KT, (int8_t*)q.p, (uint16_t*)s.p);
   e = cudaGetLastError();
   if (e == cudaSuccess) e = cudaMemcpy(codes_host, q.p, nk, cudaMemcpyDeviceToHost);
   if (e == cudaSuccess) e = cudaMemcpy(scales_host, s.p, ns * sizeof(uint16_t), cudaMemcpyDeviceToHost);
-  if (e != cudaSuccess) return fail(w, QTTS_E_CUDA, "qtts_w4_export: %s", cudaGetErrorString(e));
+  if (e != cudaSuccess) return cuda_fault(w, "qtts_w4_export", e);
   return QTTS_OK;
 }
 
@@ -811,10 +809,7 @@ int qtts_w4_linear(qtts_w4* w, int M, const uint16_t* x, int64_t x_stride, void*
   else if (4 * ((w->RB + 7) / 8 * kW4MaxSplit) >= 3 * w->G && !(w->KT >= 8 && w->KT < 16 && ctas_of(a.rw_log) <= w->G))
     e = w4_tc_launch(a, w->G, s);
   else e = w4_launch<8, 2>(a, s);
-  if (e != cudaSuccess) {
-    cudaGetLastError();  // reported here, not by the caller's next CUDA call
-    return fail(w, QTTS_E_CUDA, "qtts_w4_linear: %s", cudaGetErrorString(e));
-  }
+  if (e != cudaSuccess) return cuda_fault(w, "qtts_w4_linear", e);
   return QTTS_OK;
 }
 
