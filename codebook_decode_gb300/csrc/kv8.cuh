@@ -27,7 +27,7 @@ struct qtts_kv8 {
   qtts_kv8_config cfg{};
   int device = 0;
   int G = 0;  // SMs
-  char err[256] = {};
+  qtts::ErrorText err;
   uint8_t* codes = nullptr;
   float* scales = nullptr;
   float* rope_cos = nullptr;  // [max_context][d / 2], or nullptr: no rotation

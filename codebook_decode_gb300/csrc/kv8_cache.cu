@@ -337,12 +337,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 4)
   }
 }
 
-char g_err[256];
+thread_local ErrorText g_err;  // of calls without a handle
 
 int fail(qtts_kv8* c, int code, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
-  vsnprintf(c ? c->err : g_err, 256, fmt, ap);
+  (c ? c->err : g_err).set(fmt, ap);
   va_end(ap);
   return code;
 }
@@ -416,7 +416,7 @@ using namespace qtts;
 
 extern "C" {
 
-const char* qtts_kv8_last_error(const qtts_kv8* c) { return c ? c->err : g_err; }
+const char* qtts_kv8_last_error(const qtts_kv8* c) { return (c ? c->err : g_err).get(); }
 
 int qtts_kv8_create(const qtts_kv8_config* cfg, int device, qtts_kv8** out) {
   if (!cfg || !out) return fail(nullptr, QTTS_E_INVALID, "null argument");

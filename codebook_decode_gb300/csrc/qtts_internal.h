@@ -5,6 +5,11 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <cstdarg>
+#include <cstdio>
+#include <cstring>
+#include <mutex>
+
 #include "qtts.h"
 
 namespace qtts {
@@ -262,6 +267,24 @@ cudaError_t pf_chunk(const PfCtx& c, int B, int P, const qtts_session* sess, con
 // kernel's codebook-0 head stage reads them); kv_len is not advanced here
 cudaError_t pf_talker_step(const PfCtx& c, int B, const qtts_session* sess, const int32_t* bt, int bt_stride,
                            const uint16_t* in_embeds, uint64_t* x_words, uint32_t tag, cudaStream_t s);
+
+// The message of a handle's last failed call. Calls on one handle may come from several
+// threads: each reads a copy of its own, whole, and valid until it asks again.
+class ErrorText {
+  mutable std::mutex lock_;
+  char text_[256] = {};
+
+ public:
+  void set(const char* fmt, va_list ap) {
+    std::lock_guard<std::mutex> hold(lock_);
+    vsnprintf(text_, sizeof text_, fmt, ap);
+  }
+  const char* get() const {
+    static thread_local char copy[sizeof text_];
+    std::lock_guard<std::mutex> hold(lock_);
+    return (const char*)memcpy(copy, text_, sizeof copy);
+  }
+};
 
 // The caller's current device is put back on every path out.
 struct DeviceGuard {

@@ -34,7 +34,7 @@
 struct qtts_w4 {
   int N = 0, K = 0, group = 0, device = 0, G = 0;
   int RB = 0, KT = 0;  // row blocks of 16, k tiles of 64
-  char err[256] = {};
+  qtts::ErrorText err;
   uint4* codes = nullptr;      // [RB][KT][32 lanes]
   uint16_t* scales = nullptr;  // [RB][units][16 or 32]
   bool loaded = false;
@@ -613,12 +613,12 @@ cudaError_t w4_tc_launch(W4Args a, int sms, cudaStream_t s) {
   return cudaLaunchKernelEx(&lc, w4_tc_kernel, a);
 }
 
-char g_w4_err[256];
+thread_local ErrorText g_w4_err;  // of calls without a handle
 
 int fail(qtts_w4* w, int code, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
-  vsnprintf(w ? w->err : g_w4_err, 256, fmt, ap);
+  (w ? w->err : g_w4_err).set(fmt, ap);
   va_end(ap);
   return code;
 }
@@ -644,7 +644,7 @@ using namespace qtts;
 
 extern "C" {
 
-const char* qtts_w4_last_error(const qtts_w4* w) { return w ? w->err : g_w4_err; }
+const char* qtts_w4_last_error(const qtts_w4* w) { return (w ? w->err : g_w4_err).get(); }
 
 int qtts_w4_create(int N, int K, int group, int device, qtts_w4** out) {
   if (!out) return fail(nullptr, QTTS_E_INVALID, "null argument");

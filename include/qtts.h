@@ -443,7 +443,9 @@ typedef struct {
   int32_t pool_pages;   /* pages of every layer */
 } qtts_kv8_config;
 
-const char* qtts_kv8_last_error(const qtts_kv8* c); /* c may be NULL for create errors */
+/* The last message of a failed call on c; NULL: of this thread's last failed
+ * create. A copy of the calling thread's, valid until it asks again. */
+const char* qtts_kv8_last_error(const qtts_kv8* c);
 int qtts_kv8_create(const qtts_kv8_config* cfg, int device, qtts_kv8** out);
 void qtts_kv8_destroy(qtts_kv8* c);
 
@@ -499,7 +501,7 @@ int qtts_kv8_status(qtts_kv8* c, int* device_err);
  * ------------------------------------------------------------------------- */
 typedef struct qtts_w4 qtts_w4;
 
-const char* qtts_w4_last_error(const qtts_w4* w); /* w may be NULL for create errors */
+const char* qtts_w4_last_error(const qtts_w4* w); /* as qtts_kv8_last_error */
 /* N 1..2^24 rows (any number), K 1..2^20, a multiple of group. */
 int qtts_w4_create(int N, int K, int group, int device, qtts_w4** out);
 void qtts_w4_destroy(qtts_w4* w);
