@@ -593,7 +593,11 @@ int qtts_kv8_status(qtts_kv8* c, int* device_err) {
   int v = 0;
   cudaError_t e = cudaDeviceSynchronize();
   if (e == cudaSuccess) e = cudaMemcpy(&v, c->dev_err, sizeof(int), cudaMemcpyDeviceToHost);
-  if (e == cudaSuccess && v) e = cudaMemset(c->dev_err, 0, sizeof(int));
+  if (e == cudaSuccess && v) {
+    // waited for: other streams do not wait for it, and their errors are the next call's
+    e = cudaMemset(c->dev_err, 0, sizeof(int));
+    if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
+  }
   if (e != cudaSuccess) return cuda_fault(c, "qtts_kv8_status", e);
   if (device_err) *device_err = v;
   if (v == QTTS_DEV_TIMEOUT) return fail(c, QTTS_E_TIMEOUT, "a device-side wait ran out its limit");
