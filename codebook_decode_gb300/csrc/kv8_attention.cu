@@ -26,9 +26,9 @@
 // results do not depend on which one that is.
 //
 // Bound by bytes for long sessions (one token each of 32 sessions of 4000 to 16000,
-// 16 q and 8 kv heads of 128: 108 us, 6.1 TB/s; one of 130000: 49 us, 5.5 TB/s), by
+// 16 q and 8 kv heads of 128: 108 us, 6.1 TB/s; one of 130000: 49 us, 5.4 TB/s), by
 // the chain of lengths, table, copies, softmax and join for short ones (8 sessions of
-// 64 to 512: 8 us).
+// 64 to 512: 8 us; from tables of 16384 pages, where the tiles have to be counted first, 9).
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -750,8 +750,10 @@ cudaError_t kv8_attention(const Kv8View& v, const Kv8Batch& q, int d, int group,
   float* part = (float*)((char*)work + kCtas * (size_t)sms * sizeof(unsigned));
   // 9 to 16 columns of tiles that would be cut: the join of that many columns costs more
   // than the tensor cores' kernel while the work is small (8 rows of 2 q heads a kv head
-  // behind 1000 tokens 27 and 19 us, 16 sessions of them 30 and 20; 8 sessions behind
-  // 2000 31 and 27, behind 8000 50 and 68)
+  // behind 1000 tokens 27 and 19 us, 16 sessions of them 34 and 23; 8 sessions behind
+  // 2000 31 and 27, behind 8000 50 and 68). The host knows no lengths: pages is what the
+  // tables could hold, so short sessions in tables for long ones take the slower side (the
+  // first two from tables of 2500 pages 27 and 34 us).
   const long long tiles = (long long)q.B * v.nkv, pages = most_pages(v, q);
   const bool whole = tiles <= sms * kCtas && pages <= (2 * tiles >= sms * kCtas ? kWholePagesMany : kWholePages);
   if (cols > kMaxCols || (cols > 8 && !whole && tiles * pages <= 128ll * sms && kv8_chunk_fits(v, q, group, pages)))

@@ -107,14 +107,14 @@ __device__ __forceinline__ float new_scale(uint32_t amax, float s_old) {
   return s_old > s ? s_old : s;
 }
 
-// Append: one warp per block, everything it adds to the block in registers:
-// read the rows once, rotate (K), take the block's largest magnitude, quantise,
-// write. Bound by bytes for prompts and by latency for single tokens, so the
+// Append: one warp per block, the rows that it adds to the block in registers (of
+// which three spill at head_dim 128): read them once, rotate (K), take the block's
+// largest magnitude, quantise, write. Bound by bytes for prompts and by latency for single tokens, so the
 // rows are asked for as soon as the session's lengths are there, together with
 // the page's id and the rotation (once per CTA, in shared memory). 32 sessions of
-// 60 to 1000 tokens, 8 kv heads of 128 (105 MB): 30 us, 3.5 TB/s; half of what
-// the bytes allow goes to instructions and to the phases of a CTA (lengths, rows,
-// codes). One token of 32 sessions: 4 us.
+// 60 to 1000 tokens, 8 kv heads of 128 (105 MB): 30 us, 3.5 TB/s, where the
+// bytes would allow 15.5; the other half goes to instructions (K is rotated twice) and
+// to the phases of a CTA (lengths, rows, codes). One token of 32 sessions: 4 us.
 template <int D>
 __global__ void __launch_bounds__(kMaxWarps * 32, 2)
     append_kernel(Kv8View c, Kv8Batch q, int touched, const uint16_t* __restrict__ k, int64_t k_stride,

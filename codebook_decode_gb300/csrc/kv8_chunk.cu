@@ -25,6 +25,10 @@
 // What moved it most was code size and local memory: with the waits unrolled and
 // each role's place in the work in registers the code had 165 KB, did not stay in
 // the instruction cache, and spilled into a first-level cache of a few KB (40 us).
+// What still spills at head_dim 128 are 40 bytes a thread (20 in the 256-row form).
+//
+// A weight leaves fp32's range, and the sum, where its block's V scale is not 0 but below
+// 2^-100 of another one that counts in the same row.
 //
 // Work is cut into equal shares of key steps, one per CTA; tiles that several
 // CTAs share are joined through the workspace by the last to arrive, in order.

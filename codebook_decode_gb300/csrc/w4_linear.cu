@@ -1,9 +1,10 @@
 // w4_linear.cu -- products of up to 64 activation rows with 4-bit weights:
 // y[m][n] = sum_k x[m][k] * code[n][k] * scale[n][k / group].
 //
-// Few rows are bound by the launch, one round of loads and the instructions that
-// widen (one row: 4096 x 2048 3.7 us; 12288 x 2048 in groups of 32 6.1 us, 2.3 TB/s;
-// four rows, 30000 x 4096: 32 us, 2.0 TB/s), not by the weights' bytes. The weights are
+// Few rows are bound by the launch and one round of loads (one row, 4096 x 2048: 3.7 us;
+// 12288 x 2048 in groups of 32 6.1 us, 2.3 TB/s), large layers by short CTAs that come in
+// waves, each copying the activations before its first product (four rows, 30000 x 4096:
+// 938 CTAs in 456 places, 32 us, 2.0 TB/s), not by the weights' bytes. The weights are
 // the A operand of mma.sync m16n8k16 (16 output columns of the layer per
 // tile), the activations the B operand (8 rows per n-tile), so that one
 // activation row pads to 8, not to 16 or 128. Codes are exact in bf16 and are

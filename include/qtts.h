@@ -449,14 +449,14 @@ const char* qtts_kv8_last_error(const qtts_kv8* c);
 int qtts_kv8_create(const qtts_kv8_config* cfg, int device, qtts_kv8** out);
 void qtts_kv8_destroy(qtts_kv8* c);
 
-/* The page pool, as qtts_kv_alloc_pages and its kind. */
+/* The page pool, as qtts_kv_alloc_pages and its kind: one thread at a time. */
 int qtts_kv8_alloc_pages(qtts_kv8* c, int n, int32_t* ids_host);
 int qtts_kv8_free_pages(qtts_kv8* c, int n, const int32_t* ids_host);
 int qtts_kv8_free_count(const qtts_kv8* c);
 
 /* Append n rows per session to layer `layer`: K rotated by its position
  * (rotate-half pairs (i, i + d/2) by pos * theta^(-2i/d), angles in double,
- * products in fp32), then K and V quantised into the pages. k, v: rows of
+ * cosine and sine in fp32, a product and a fused multiply-add in fp32), then K and V quantised into the pages. k, v: rows of
  * [n_kv_heads][head_dim]. No two sessions of a call may append to the same
  * page (they would write the same block); sharing pages that are only read is
  * fine. */
@@ -469,7 +469,16 @@ int qtts_kv8_append(qtts_kv8* c, int layer, int B, int n_rows, int max_new, cons
  *   out = sum_j softmax_j(scale * q_rot . K_j) V_j
  * q: rows of [n_q_heads][head_dim], not yet rotated (they are rotated like K
  * here, in fp32); out: the same shape. Query head h reads kv head
- * h / (n_q_heads / n_kv_heads). out must not overlap q. workspace:
+ * h / (n_q_heads / n_kv_heads). out must not overlap q.
+ * Queries (after the rotation) are rounded to half (11 bits) at a power of two
+ * of their row's largest magnitude, weights times V scale to half at about the
+ * largest of them; codes are exact in half; scores, maxima, sums and products
+ * are fp32, the result is rounded once. V scales of one session should lie
+ * within 2^100 of each other (blocks of zeros aside).
+ * n_rows, max_new and bt_stride also choose the kernel, so results may differ
+ * in rounding with them, and bounds far above what the sessions have cost time:
+ * max_new above all (32 sessions of one token, 100 to 1200 back: 16 us with 1,
+ * 22 with 8, 55 with 64). workspace:
  * qtts_kv8_workspace_bytes (41 MB at head_dim 128, 21 at 64) of device
  * memory, 16-byte aligned, zeroed once before its first call and left ready
  * for the next one; calls that may overlap (on several streams, or captured
@@ -522,7 +531,8 @@ int qtts_w4_export(qtts_w4* w, int8_t* codes_host, uint16_t* scales_host);
  * aligned, x_stride elements between rows (a multiple of 8); y: device
  * [M][N], bf16 (QTTS_DTYPE_BF16, rounded once) or fp32 (QTTS_DTYPE_F32),
  * y_stride elements between rows. x and y must not overlap. Asynchronous on
- * `stream`, allocates nothing, can be captured into a graph. */
+ * `stream`, allocates nothing, can be captured into a graph. A device-side wait
+ * that runs out its limit leaves NaN in the results that it is about. */
 int qtts_w4_linear(qtts_w4* w, int M, const uint16_t* x, int64_t x_stride, void* y, int64_t y_stride, int y_dtype,
                    void* stream);
 
